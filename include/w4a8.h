@@ -73,11 +73,11 @@ typedef enum {
 #define W4A8_DEVERR_EPILOGUE_WAIT 4
 #define W4A8_DEVERR_DRAIN_WAIT 5
 #define W4A8_DEVERR_SELFTEST_WAIT 6
-#define W4A8_DEVERR_KV_RANGE 7 /* a KV-cache length or position outside [0, Lmax] (clamped or skipped) */
+#define W4A8_DEVERR_KV_RANGE 7 /* a KV-cache length, position or page outside its range (clamped or skipped) */
 #define W4A8_DEVERR_PACK_RANGE 8 /* a packer met a code, zero point or scale outside its documented range */
 #define W4A8_DEVERR_CHAIN_WAIT 9 /* w4a8_chain: a wait on another CTA's progress gave up */
 #define W4A8_DEVERR_BOUNDS 10     /* debug builds (W4A8_DEBUG) only: an access outside its buffer was skipped */
-#define W4A8_DEVERR_KV_WAIT 11    /* w4kv_attention_decode: a chunk's cache copies did not land in time */
+#define W4A8_DEVERR_KV_WAIT 11    /* KV-cache attention: cache copies or products were not done in time */
 
 /* Human-readable name of a status code (static string, never NULL). */
 W4A8_API const char* w4a8_status_string(int status);
@@ -479,6 +479,117 @@ W4A8_API w4a8_status_t w4kv_attention_decode(const void* q, const uint8_t* k_cod
                                              const int32_t* seq_lens, int64_t B, int64_t Hq, int64_t Hkv,
                                              int64_t Lmax, int32_t D, float scale, void* out, void* workspace,
                                              size_t workspace_bytes, w4a8_stream_t stream);
+
+/*
+ * Residual addition, root-mean-square norm and int8 quantization in one
+ * launch: what stands between two linear layers of a W4A8 model
+ * ("QServe/QoQ" abstract: W4A8 serving). For each row m:
+ *   h[m,k] = fp16_rn(X[m,k] + residual[m,k])   (h = X without a residual)
+ *   y[m,k] = h[m,k] * (1 / sqrt(mean_k h[m,k]^2 + eps)) * weight[k]   (fp32)
+ *   sA[m]  = fp16_rn(max_k |y[m,k]| / 127)
+ *   A8[m,k] = clamp(rint(y[m,k] / float(sA[m])), -127, 127)
+ *   sA[m] == 0 gives A8[m,:] = 0;  rowsum[m] = sum_k A8[m,k].
+ * (A8, sA, rowsum) feed w4a8_gemm as those of w4a8_quantize_act do. The
+ * quantizer works on the fp32 values of y; the norm on the rounded h, so that
+ * a call on h alone gives the same codes.
+ * X, residual: fp16 [M, K] (16-byte aligned); residual may be NULL, and H is
+ * NULL exactly then. H: fp16 [M, K], h; it may be X or residual itself.
+ * weight: fp16 [K] (16-byte aligned). eps >= 0. A8, sA, rowsum and the limits
+ * as for w4a8_quantize_act. Non-finite inputs, or an h beyond fp16, are a
+ * precondition violation (that row's codes unspecified).
+ */
+W4A8_API w4a8_status_t w4a8_rmsnorm_quantize_act(const void* X, const void* residual, const void* weight, float eps,
+                                                 int64_t M, int64_t K, void* H, int8_t* A8, void* sA,
+                                                 int32_t* rowsum, w4a8_stream_t stream);
+
+/*
+ * Paged 8-bit KV cache. Codes are int8 [num_pages, 2, Hkv, page, 128] (128-byte
+ * aligned; second index 0 = K, 1 = V), with one fp32 scale per (page, K | V,
+ * head): scales [num_pages, 2, Hkv] (4-byte aligned). Value = code * scale.
+ * Token p of sequence b is at place p % page of page block_table[b, p / page]
+ * (int32 [B, max_blocks], 4-byte aligned); sequences may share pages that a
+ * call only reads. Entries for positions at or beyond a sequence's length are
+ * not looked at.
+ * Limits: D == 128; page 16, 32, 64 or 128; 1 <= Hkv, Hq % Hkv == 0, Hq <=
+ * 1024; max_blocks * page <= 2^24; num_pages * 2 * Hkv * page < 2^31; B <= 65535.
+ *
+ * A batch is B sequences with T rows (new tokens) in all. Sequence b's rows
+ * are q_start[b] .. q_start[b + 1] - 1 (int32 [B + 1], device memory, not
+ * falling, within [0, T]), its length after them seq_lens[b] (int32 [B],
+ * device memory): its new tokens are its last ones. q_start NULL means one row
+ * per sequence (T == B), a sequence of length 0 then being an unused place of
+ * the batch. Rows that belong to no sequence are left as they are in every
+ * output. A length above max_blocks * page or below the number of new tokens,
+ * and a page outside [0, num_pages), are recorded as W4A8_DEVERR_KV_RANGE: the
+ * append skips the tokens concerned, the attention gives values of that
+ * sequence that mean nothing; no access leaves the buffers.
+ */
+typedef struct {
+  int8_t* codes;
+  float* scales;
+  const int32_t* block_table;
+  int64_t num_pages, max_blocks;
+  int32_t Hkv, page, D;
+  int32_t reserved; /* must be 0 */
+} w4a8_kv8_cache_t;
+
+/*
+ * Rotary positions and the append. qkv: fp16 [T, (Hq + 2 Hkv) * 128] (16-byte
+ * aligned), rows of q, k and v heads as the GEMM of the joint projection
+ * writes them. The first rotary_dim values (even, 0 .. 128) of every q and k
+ * head are rotated by the token's position p = seq_lens[b] - n_b + i: pairs (2
+ * j, 2 j + 1) if interleaved, else (j, j + rotary_dim / 2),
+ *   (a, b) -> rope_scale * (a cos t - b sin t, a sin t + b cos t),  t = p * inv_freq[j],
+ * the angle exact to 2^-24 radians at every position (no fp32 product of a
+ * large position). inv_freq: fp32 [rotary_dim / 2] in device memory, as scaled
+ * for long contexts by the caller; rope_scale: a factor on the rotated values
+ * (1 for none).
+ * q goes to q_out, fp16 [T, Hq, 128] (16-byte aligned); k and v (as fp32, not
+ * rounded in between) into the cache. In every page that gets new tokens
+ *   s' = max(s, fp32(max |new values| / 127)),  s = 0 if the page's first place is one of them
+ *   codes that were there: rint(code * (s / s')) if s' > s
+ *   new codes: clamp(rint(x / s'), -127, 127)   (IEEE divides, ties to even; s' == 0 gives zeros)
+ * and s' becomes its scale. Places behind the new tokens are left as they are.
+ * A page that gets new tokens must not be shared with another sequence of the
+ * batch. Non-finite inputs are a precondition violation (that page's contents
+ * unspecified).
+ */
+W4A8_API w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cache_t* cache, const int32_t* seq_lens,
+                                            const int32_t* q_start, int64_t B, int64_t T, int64_t Hq,
+                                            const float* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                                            float rope_scale, void* q_out, w4a8_stream_t stream);
+
+/* Workspace bytes of the attention calls below (0 if the sizes are
+ * unsupported); it does not depend on the lengths. */
+W4A8_API size_t w4a8_kv8_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv);
+
+/*
+ * Attention of one new token per sequence over the cache that already holds
+ * it. q, out: fp16 [B, Hq, 128] (16-byte aligned). Query head h reads kv head
+ * h / (Hq / Hkv);
+ *   s_j = scale * sK * sum_d q[d] * codeK[j, d],  j < seq_lens[b]
+ *   out[b, h] = fp16_rn(sum_j softmax(s)_j * sV * codeV[j])
+ * with sK, sV the scales of j's page, in fp32; seq_lens[b] == 0 gives zeros.
+ * workspace: 256-byte aligned, at least w4a8_kv8_attention_workspace_bytes(B,
+ * B, Hq, Hkv) bytes, zero-filled by the caller once; every call that completes
+ * without a device error leaves its counters zero again. Calls that share a
+ * workspace must not overlap on the GPU.
+ */
+W4A8_API w4a8_status_t w4a8_kv8_attention_decode(const void* q, const w4a8_kv8_cache_t* cache,
+                                                 const int32_t* seq_lens, int64_t B, int64_t Hq, float scale,
+                                                 void* out, void* workspace, size_t workspace_bytes,
+                                                 w4a8_stream_t stream);
+
+/*
+ * The same for several new tokens per sequence (q_start as above, required),
+ * causal: row i of sequence b's n_b rows sees its tokens j < seq_lens[b] - n_b
+ * + i + 1. q, out: fp16 [T, Hq, 128]. workspace as for the decode call, of
+ * w4a8_kv8_attention_workspace_bytes(B, T, Hq, Hkv) bytes.
+ */
+W4A8_API w4a8_status_t w4a8_kv8_attention_prefill(const void* q, const w4a8_kv8_cache_t* cache,
+                                                  const int32_t* seq_lens, const int32_t* q_start, int64_t B,
+                                                  int64_t T, int64_t Hq, float scale, void* out, void* workspace,
+                                                  size_t workspace_bytes, w4a8_stream_t stream);
 
 /*
  * Allocation-free GEMM: the same computation and results as w4a8_gemm, for

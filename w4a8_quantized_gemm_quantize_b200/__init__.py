@@ -22,7 +22,8 @@ __all__ = [
     "selftest_bounded_wait", "quantize_act_static", "w4a4_quantize_act", "w4a4_quantize_act_static",
     "w4a4_gemm", "w4a4_gemm_ex", "w4a4_workspace_bytes", "lut_packed_bytes", "lut_pack_weights", "lut_gemm",
     "lut_gemm_ex", "lut3_packed_bytes", "lut3_pack_weights", "lut3_gemm", "lut3_gemm_ex", "kv4_quantize", "kv4_append", "kv4_workspace_bytes", "kv4_attention_decode",
-    "ChainLink", "chain_links", "chain_workspace_bytes", "chain",
+    "ChainLink", "chain_links", "chain_workspace_bytes", "chain", "rmsnorm_quantize_act", "kv8_cache",
+    "rope_frequencies", "kv8_rope_append", "kv8_workspace_bytes", "kv8_attention_decode", "kv8_attention_prefill",
 ]
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -38,6 +39,8 @@ EXPORTED_SYMBOLS = (
     "w4kv_quantize", "w4kv_append", "w4kv_attention_workspace_bytes", "w4kv_attention_decode",
     "w4lut3_packed_bytes", "w4lut3_pack_weights", "w4lut3_gemm", "w4lut3_gemm_ex",
     "w4a8_chain_workspace_bytes", "w4a8_chain",
+    "w4a8_rmsnorm_quantize_act", "w4a8_kv8_rope_append", "w4a8_kv8_attention_workspace_bytes",
+    "w4a8_kv8_attention_decode", "w4a8_kv8_attention_prefill",
 )
 
 SCHEDULE_AUTO, SCHEDULE_WHOLE_TILES, SCHEDULE_SPLIT_K, SCHEDULE_CLUSTER = 0, 1, 2, 3
@@ -57,6 +60,13 @@ class ChainLink(ctypes.Structure):
     _fields_ = [("A", ctypes.c_void_p), ("packed", ctypes.c_void_p), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64), ("A8", ctypes.c_void_p), ("sA", ctypes.c_void_p), ("rowsum", ctypes.c_void_p),
                 ("Y", ctypes.c_void_p)]
+
+
+class Kv8CacheDesc(ctypes.Structure):
+    """w4a8_kv8_cache_t: a paged 8-bit KV cache and a batch's block table."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("max_blocks", ctypes.c_int64), ("Hkv", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("D", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -110,6 +120,14 @@ def lib() -> ctypes.CDLL:
                                                  vp, vp, sz, vp]),
         "w4a8_chain_workspace_bytes": (sz, [ctypes.POINTER(ChainLink), i32]),
         "w4a8_chain": (ctypes.c_int, [ctypes.POINTER(ChainLink), i32, vp, sz, vp]),
+        "w4a8_rmsnorm_quantize_act": (ctypes.c_int, [vp, vp, vp, ctypes.c_float, i64, i64, vp, vp, vp, vp, vp]),
+        "w4a8_kv8_rope_append": (ctypes.c_int, [vp, ctypes.POINTER(Kv8CacheDesc), vp, vp, i64, i64, i64, vp, i32, i32,
+                                                ctypes.c_float, vp, vp]),
+        "w4a8_kv8_attention_workspace_bytes": (sz, [i64, i64, i64, i64]),
+        "w4a8_kv8_attention_decode": (ctypes.c_int, [vp, ctypes.POINTER(Kv8CacheDesc), vp, i64, i64, ctypes.c_float,
+                                                     vp, vp, sz, vp]),
+        "w4a8_kv8_attention_prefill": (ctypes.c_int, [vp, ctypes.POINTER(Kv8CacheDesc), vp, vp, i64, i64, i64,
+                                                      ctypes.c_float, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -640,3 +658,244 @@ def chain(links, workspace):
     ws_bytes = workspace.numel() * workspace.element_size()
     dev = workspace.device
     _check(lib().w4a8_chain(arr, len(arr), _ptr(workspace), ws_bytes, _stream(dev)), "w4a8_chain")
+
+
+# ------------------------------------------- between the GEMMs of a decoder layer
+# These run once or more per layer and step, so their host side is kept short:
+# plain integers for pointers, and the device is switched only when it differs.
+def _check_tensor(t, name, dtype, device, shape=None):
+    """One argument: CUDA, contiguous, of this type, device and shape (None in a shape: any)."""
+    if not t.is_cuda:
+        raise W4A8Error("tensors must live on a CUDA device (no CPU path exists)")
+    if not t.is_contiguous():
+        raise W4A8Error("tensors must be contiguous")
+    if t.dtype is not dtype or t.device != device or (shape is not None and t.shape != shape):
+        want = "" if shape is None else f" {list(shape)}"
+        raise W4A8Error(f"{name} must be {str(dtype).replace('torch.', '')}{want} on {device}, got "
+                        f"{str(t.dtype).replace('torch.', '')} {list(t.shape)} on {t.device}")
+
+
+def _launch(device, what, fn, *args):
+    """Calls fn(*args, stream) on the device's current stream, with that device current."""
+    torch = _torch()
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, stream)
+    if code != 0:
+        raise W4A8Error(f"{what}: {status_string(code)}")
+
+
+def rmsnorm_quantize_act(X, weight, eps, residual=None, out=None):
+    """Residual addition, root-mean-square norm and per-token int8
+    quantization: X and residual fp16 [M, K], weight fp16 [K] -> (H fp16
+    [M, K] = X + residual (None without a residual), A8 int8 [M, K], sA fp16
+    [M], rowsum int32 [M]); the last three feed gemm. out: the four outputs
+    (the first may be X or residual, and is not looked at without a residual)."""
+    torch = _torch()
+    dev = X.device
+    if X.dim() != 2:
+        raise W4A8Error("X must be a 2-D fp16 tensor")
+    M, K = X.shape
+    f16 = torch.float16
+    _check_tensor(X, "X", f16, dev)
+    _check_tensor(weight, "weight", f16, dev, (K,))
+    if out is None:
+        H = None if residual is None else torch.empty_like(X)
+        A8 = torch.empty((M, K), dtype=torch.int8, device=dev)
+        sA = torch.empty((M,), dtype=f16, device=dev)
+        rowsum = torch.empty((M,), dtype=torch.int32, device=dev)
+    else:
+        H, A8, sA, rowsum = out
+        _check_tensor(A8, "A8", torch.int8, dev, (M, K))
+        _check_tensor(sA, "sA", f16, dev, (M,))
+        _check_tensor(rowsum, "rowsum", torch.int32, dev, (M,))
+    if residual is None:
+        H, r, h = None, None, None
+    else:
+        _check_tensor(residual, "residual", f16, dev, (M, K))
+        _check_tensor(H, "H", f16, dev, (M, K))
+        r, h = residual.data_ptr(), H.data_ptr()
+    _launch(dev, "w4a8_rmsnorm_quantize_act", lib().w4a8_rmsnorm_quantize_act, X.data_ptr(), r, weight.data_ptr(), eps,
+            M, K, h, A8.data_ptr(), sA.data_ptr(), rowsum.data_ptr())
+    return H, A8, sA, rowsum
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: int = 8192, low: float | None = None, high: float | None = None, device=None):
+    """Rotation per position of each pair, fp32 [rotary_dim / 2], and the
+    factor on the rotated values, for kv8_rope_append: base^(-2 j / rotary_dim),
+    for contexts `factor` times longer than the original_length trained on:
+
+    * "none"    as they are;
+    * "linear"  all divided by factor (positions stretched);
+    * "bands"   pairs that turn fewer than `low` (1) times within the original
+      length divided by factor, more than `high` (4) times kept, blended in
+      between by the number of turns;
+    * "ramp"    the same with the blend linear in the pair's index, between
+      those that turn `high` (32) times and `low` (1) once, and the rotated
+      values scaled by 0.1 ln(factor) + 1."""
+    torch = _torch()
+    import math
+    if rotary_dim < 0 or rotary_dim > KV_HEAD_DIM or rotary_dim % 2:
+        raise W4A8Error("rotary_dim must be even, 0..128")
+    if base <= 0 or factor < 1 or original_length <= 0:
+        raise W4A8Error("base and original_length must be positive, factor at least 1")
+    n = rotary_dim // 2
+    f = [base ** (-2.0 * j / rotary_dim) for j in range(n)]
+    ms = 1.0
+    if scaling == "none":
+        pass
+    elif scaling == "linear":
+        f = [x / factor for x in f]
+    elif scaling == "bands":
+        lo, hi = 1.0 if low is None else low, 4.0 if high is None else high
+        if not 0 < lo < hi:
+            raise W4A8Error("0 < low < high is wanted")
+        keep = [min(1.0, max(0.0, (original_length * x / (2 * math.pi) - lo) / (hi - lo))) for x in f]
+        f = [k * x + (1 - k) * x / factor for k, x in zip(keep, f)]
+    elif scaling == "ramp":
+        lo, hi = 1.0 if low is None else low, 32.0 if high is None else high
+        if not 0 < lo < hi or base == 1.0:
+            raise W4A8Error("0 < low < high and a base other than 1 are wanted")
+
+        def pair_of(turns):
+            return rotary_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+        a, b = max(math.floor(pair_of(hi)), 0), min(math.ceil(pair_of(lo)), rotary_dim - 1)
+        stretch = [min(1.0, max(0.0, (j - a) / max(b - a, 1e-3))) for j in range(n)]
+        f = [t * x / factor + (1 - t) * x for t, x in zip(stretch, f)]
+        ms = 0.1 * math.log(factor) + 1.0
+    else:
+        raise W4A8Error(f"unknown scaling {scaling!r}")
+    return torch.tensor(f, dtype=torch.float64).to(torch.float32).to(device), ms
+
+
+def kv8_cache(num_pages: int, Hkv: int, page: int = 64, device=None):
+    """An empty paged 8-bit KV cache: codes int8 [num_pages, 2, Hkv, page,
+    128] and scales fp32 [num_pages, 2, Hkv]."""
+    torch = _torch()
+    if page not in (16, 32, 64, 128) or num_pages < 1 or Hkv < 1:
+        raise W4A8Error("page must be 16, 32, 64 or 128, num_pages and Hkv positive")
+    return (torch.zeros((num_pages, 2, Hkv, page, KV_HEAD_DIM), dtype=torch.int8, device=device),
+            torch.zeros((num_pages, 2, Hkv), dtype=torch.float32, device=device))
+
+
+def _kv8_desc(codes, scales, block_table, seq_lens, device):
+    """The cache descriptor of a call, its tensors checked."""
+    torch = _torch()
+    if codes.dim() != 5 or block_table.dim() != 2:
+        raise W4A8Error("kv_codes must be int8 [num_pages, 2, Hkv, page, 128] and block_table int32 [B, max_blocks]")
+    pages, two, Hkv, page, D = codes.shape
+    if two != 2:
+        raise W4A8Error("kv_codes must be int8 [num_pages, 2, Hkv, page, 128]")
+    i32 = torch.int32
+    _check_tensor(codes, "kv_codes", torch.int8, device)
+    _check_tensor(scales, "kv_scales", torch.float32, device, (pages, 2, Hkv))
+    _check_tensor(block_table, "block_table", i32, device)
+    B, blocks = block_table.shape
+    _check_tensor(seq_lens, "seq_lens", i32, device, (B,))
+    return Kv8CacheDesc(codes.data_ptr(), scales.data_ptr(), block_table.data_ptr(), pages, blocks, Hkv, page, D,
+                        0), B, Hkv
+
+
+def kv8_rope_append(qkv, Hq: int, kv_codes, kv_scales, block_table, seq_lens, inv_freq, q_start=None,
+                    interleaved: bool = False, rope_scale: float = 1.0, out=None):
+    """Rotates q and k of qkv fp16 [T, (Hq + 2 Hkv) * 128] at their tokens'
+    positions, returns q fp16 [T, Hq, 128] and appends k and v to the paged
+    8-bit cache. seq_lens int32 [B]: each sequence's length with its new tokens;
+    q_start int32 [B + 1]: its first new row (None: one row per sequence).
+    inv_freq fp32 [rotary_dim / 2] and rope_scale as from rope_frequencies."""
+    torch = _torch()
+    dev = qkv.device
+    desc, B, Hkv = _kv8_desc(kv_codes, kv_scales, block_table, seq_lens, dev)
+    if qkv.dim() != 2:
+        raise W4A8Error("qkv must be fp16 [T, (Hq + 2 Hkv) * 128]")
+    T = qkv.shape[0]
+    f16 = torch.float16
+    _check_tensor(qkv, "qkv", f16, dev, (T, (Hq + 2 * Hkv) * KV_HEAD_DIM))
+    _check_tensor(inv_freq, "inv_freq", torch.float32, dev)
+    if q_start is None:
+        start = None
+    else:
+        _check_tensor(q_start, "q_start", torch.int32, dev, (B + 1,))
+        start = q_start.data_ptr()
+    if out is None:
+        out = torch.empty((T, Hq, KV_HEAD_DIM), dtype=f16, device=dev)
+    else:
+        _check_tensor(out, "out", f16, dev, (T, Hq, KV_HEAD_DIM))
+    _launch(dev, "w4a8_kv8_rope_append", lib().w4a8_kv8_rope_append, qkv.data_ptr(), desc, seq_lens.data_ptr(), start,
+            B, T, Hq, inv_freq.data_ptr(), 2 * inv_freq.numel(), 1 if interleaved else 0, rope_scale, out.data_ptr())
+    return out
+
+
+def kv8_workspace_bytes(B: int, T: int, Hq: int, Hkv: int) -> int:
+    return int(lib().w4a8_kv8_attention_workspace_bytes(B, T, Hq, Hkv))
+
+
+_kv8_ws = {}
+
+
+def _kv8_workspace_for(device, nbytes: int):
+    """A zero-filled workspace per stream (calls on different streams may
+    overlap), grown on demand and reused; a call that is being captured gets
+    one of its own, which its graph zero-fills and keeps."""
+    torch = _torch()
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    ws = _kv8_ws.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _kv8_ws[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    return ws
+
+
+def _kv8_attention(what, q, kv_codes, kv_scales, block_table, seq_lens, scale, q_start, out, workspace):
+    torch = _torch()
+    dev = q.device
+    desc, B, Hkv = _kv8_desc(kv_codes, kv_scales, block_table, seq_lens, dev)
+    if q.dim() != 3 or q.shape[2] != KV_HEAD_DIM or (q_start is None and q.shape[0] != B):
+        raise W4A8Error("q must be fp16 [T, Hq, 128], with one row per sequence for decode")
+    T, Hq, _ = q.shape
+    f16 = torch.float16
+    _check_tensor(q, "q", f16, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_tensor(out, "out", f16, dev, q.shape)
+    L = lib()
+    if workspace is None:
+        workspace = _kv8_workspace_for(dev, max(L.w4a8_kv8_attention_workspace_bytes(B, T, Hq, Hkv), 256))
+    else:
+        _check_tensor(workspace, "workspace", torch.uint8, dev)
+    if q_start is None:
+        _launch(dev, what, L.w4a8_kv8_attention_decode, q.data_ptr(), desc, seq_lens.data_ptr(), B, Hq, scale,
+                out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    else:
+        _check_tensor(q_start, "q_start", torch.int32, dev, (B + 1,))
+        _launch(dev, what, L.w4a8_kv8_attention_prefill, q.data_ptr(), desc, seq_lens.data_ptr(), q_start.data_ptr(),
+                B, T, Hq, scale, out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def kv8_attention_decode(q, kv_codes, kv_scales, block_table, seq_lens, scale, out=None, workspace=None):
+    """Attention of one new token per sequence, q fp16 [B, Hq, 128], over the
+    paged 8-bit cache that holds it (seq_lens int32 [B]) -> fp16 [B, Hq, 128].
+    workspace: zero-filled uint8 of kv8_workspace_bytes(B, B, Hq, Hkv) (one
+    per stream is kept here if none is given); calls that share it must not
+    overlap on the GPU."""
+    return _kv8_attention("w4a8_kv8_attention_decode", q, kv_codes, kv_scales, block_table, seq_lens, scale, None,
+                          out, workspace)
+
+
+def kv8_attention_prefill(q, kv_codes, kv_scales, block_table, seq_lens, q_start, scale, out=None, workspace=None):
+    """Causal attention of several new tokens per sequence, q fp16 [T, Hq,
+    128] with sequence b's rows q_start[b] .. q_start[b + 1] - 1 (int32
+    [B + 1]), over the cache that holds them (seq_lens int32 [B]) -> fp16 [T,
+    Hq, 128]. workspace as for kv8_attention_decode, of
+    kv8_workspace_bytes(B, T, Hq, Hkv)."""
+    if q_start is None:
+        raise W4A8Error("q_start is required")
+    return _kv8_attention("w4a8_kv8_attention_prefill", q, kv_codes, kv_scales, block_table, seq_lens, scale, q_start,
+                          out, workspace)

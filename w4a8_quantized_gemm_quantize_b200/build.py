@@ -27,7 +27,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libw4a8.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libw4a8_debug.so")
-SOURCES = ["w4a8_api.cu"]
+SOURCES = ["library.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

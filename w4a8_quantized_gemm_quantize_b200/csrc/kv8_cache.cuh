@@ -1,0 +1,295 @@
+// The paged 8-bit KV cache: its layout, where a sequence's tokens lie in it,
+// and the kernel that rotates q and k and appends k and v.
+//
+// Cache: pages of P tokens (16, 32, 64 or 128), codes int8 [num_pages, 2 (K,
+// V), Hkv, P, 128], one fp32 scale per (page, K | V, head); value = code *
+// scale. Token p of sequence b lies in page block_table[b, p / P] at place p %
+// P. A scale for each block of tokens and head keeps the parameters at 1/2048
+// of the codes' bytes (P = 64) and lets attention take the scale out of whole
+// tiles of the products.
+//
+// Appending: the page's scale grows to s' = max(s, max |x| / 127) over the new
+// tokens of the page, and where it grows the codes already in the page are
+// carried over, c' = rint(c * (s / s')). A page whose first place is written
+// by the call starts from s = 0, whatever its last owner left there.
+#pragma once
+#include "ptx.cuh"
+
+namespace w4a8 {
+
+constexpr int kKv8D = 128;          // head dimension
+constexpr int kErrKv8Range = 7;     // W4A8_DEVERR_KV_RANGE
+constexpr int kErrKv8Wait = 11;     // W4A8_DEVERR_KV_WAIT
+
+struct Kv8Cache {
+  int8_t* codes;         // [num_pages, 2, Hkv, P, 128]
+  float* scales;         // [num_pages, 2, Hkv]
+  const int32_t* table;  // [B, max_blocks]
+  int num_pages, max_blocks, Hkv, P;
+};
+
+// Which sequence a row of the batch belongs to, and where it stands in it.
+struct Kv8Batch {
+  const int32_t* seq_lens;  // [B] cached tokens, the new ones among them
+  const int32_t* q_start;   // [B + 1] first new token of each sequence; null: one each
+  int B;
+  int T;  // rows
+};
+
+__device__ __forceinline__ int kv8_row_start(const Kv8Batch& s, int b) {
+  return s.q_start == nullptr ? b : min(max(__ldg(s.q_start + b), 0), s.T);
+}
+
+// Largest b in [0, B) with start_b * mul / div + b * add <= x, or -1 (the left
+// side does not fall in b). log2(B) dependent loads.
+__device__ __forceinline__ int kv8_find(const Kv8Batch& s, int64_t x, int mul, int div, int add) {
+  int lo = -1, hi = s.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    const int64_t key = static_cast<int64_t>(kv8_row_start(s, mid)) * mul / div + static_cast<int64_t>(mid) * add;
+    if (key <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Rows [first, first + n) of the batch are sequence b's new tokens, at
+// positions [pos0, pos0 + n) of it. n < 0: nothing to do; a length or a start
+// outside its range is reported.
+struct Kv8Seq {
+  int first, n, pos0, len;
+};
+__device__ __forceinline__ Kv8Seq kv8_sequence(const Kv8Batch& s, int b, int64_t capacity, int* err) {
+  Kv8Seq q;
+  q.first = kv8_row_start(s, b);
+  q.n = s.q_start == nullptr ? 1 : kv8_row_start(s, b + 1) - q.first;
+  q.len = __ldg(s.seq_lens + b);
+  if (s.q_start == nullptr && q.len == 0) q.n = 0;  // a place of the batch that no sequence fills
+  q.pos0 = q.len - q.n;
+  if (q.n < 0 || q.len < 0 || q.len > capacity || q.pos0 < 0) {
+    if (err != nullptr) atomicCAS(err, 0, kErrKv8Range);
+    q.n = -1;
+  }
+  return q;
+}
+
+// --------------------------------------------------------------- append
+struct Kv8AppendArgs {
+  const __half* qkv;  // [T, (Hq + 2 Hkv) * 128]
+  Kv8Cache c;
+  Kv8Batch s;
+  const float* inv_freq;  // [rotary / 2]
+  __half* q_out;          // [T, Hq, 128]
+  int Hq, rotary, interleaved, q_rows, q_blocks;
+  float rope_scale;
+  int* err;
+};
+
+constexpr int kKv8AppendThreads = 256;
+
+// The rotation of pair i at position pos: angle pos * f_i, taken in turns.
+// f_i / (2 pi) is held as a 64-bit fraction of a turn, so that the product
+// with the position wraps at whole turns by itself and is exact to 2^-29 of a
+// turn at position 2^24 (an fp32 product is off by 2^-24 * pos * f radians,
+// 0.008 at position 131072). Its top 32 bits give the angle in half turns.
+__device__ __forceinline__ uint64_t kv8_turns(float f) {
+  const double t = static_cast<double>(f) * 0.15915494309189533577;  // 1 / (2 pi)
+  return static_cast<uint64_t>((t - floor(t)) * 18446744073709551616.0);
+}
+__device__ __forceinline__ float2 kv8_cos_sin(uint64_t turns, int pos, float scale) {
+  const int32_t top = static_cast<int32_t>((turns * static_cast<uint64_t>(pos)) >> 32);
+  float s, c;
+  sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+  return make_float2(c * scale, s * scale);
+}
+
+// Elements 8 i .. 8 i + 7 of one head's vector (`vec` points at its 128
+// values), rotated: (a, b) -> (a cos - b sin, a sin + b cos) for the pairs (2
+// j, 2 j + 1) (interleaved) or (j, j + rotary / 2). cs: this token's (cos, sin).
+__device__ __forceinline__ void kv8_rotated(const __half* vec, int i, const float2* cs, int rotary, int interleaved,
+                                            float (&o)[8]) {
+  const uint4 raw = *reinterpret_cast<const uint4*>(vec + 8 * i);
+  const __half2* h = reinterpret_cast<const __half2*>(&raw);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(h[j]);
+    o[2 * j] = f.x;
+    o[2 * j + 1] = f.y;
+  }
+  if (8 * i >= rotary) return;
+  const int half = rotary >> 1;
+  if (interleaved) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (8 * i + 2 * j < rotary) {
+        const float2 t = cs[4 * i + j];
+        const float a = o[2 * j], b = o[2 * j + 1];
+        o[2 * j] = a * t.x - b * t.y;
+        o[2 * j + 1] = a * t.y + b * t.x;
+      }
+    }
+    return;
+  }
+  float p[8];
+  if ((half & 7) == 0) {  // the partners are another whole vector
+    const bool low = 8 * i < half;
+    const uint4 raw2 = *reinterpret_cast<const uint4*>(vec + 8 * i + (low ? half : -half));
+    const __half2* h2 = reinterpret_cast<const __half2*>(&raw2);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(h2[j]);
+      p[2 * j] = f.x;
+      p[2 * j + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int d = 8 * i + e;
+      p[e] = d < half ? __half2float(vec[d + half]) : d < rotary ? __half2float(vec[d - half]) : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int d = 8 * i + e;
+    if (d < half) {
+      const float2 t = cs[d];
+      o[e] = o[e] * t.x - p[e] * t.y;
+    } else if (d < rotary) {
+      const float2 t = cs[d - half];
+      o[e] = p[e] * t.y + o[e] * t.x;
+    }
+  }
+}
+
+// Blocks [0, q_blocks): q_rows rows of q each, every head of them (the angles
+// are worked out once a row). The others: one (page of a sequence, K | V,
+// head) each; P * 16 vectors of 8 values, in registers from the read to the
+// codes, so that the maximum over the page comes before the first code.
+template <int P>
+__global__ void __launch_bounds__(kKv8AppendThreads) kv8_append_kernel(Kv8AppendArgs a) {
+  constexpr int kSlab = kKv8AppendThreads / 16;  // tokens of the page a pass covers
+  constexpr int kPasses = P / kSlab;
+  __shared__ float2 s_cs[kSlab][kKv8D / 2];  // (cos, sin) of a slab's tokens
+  __shared__ float s_red[kKv8AppendThreads / 32];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int t = threadIdx.x;
+  const int half = a.rotary >> 1;
+  const int64_t capacity = static_cast<int64_t>(a.c.max_blocks) * P;
+  const int64_t row_elems = static_cast<int64_t>(a.Hq + 2 * a.c.Hkv) * kKv8D;
+  if (static_cast<int>(blockIdx.x) < a.q_blocks) {
+    for (int k = 0; k < a.q_rows; ++k) {
+      const int row = static_cast<int>(blockIdx.x) * a.q_rows + k;
+      if (row >= a.s.T) break;
+      const int b = a.s.q_start == nullptr ? row : kv8_find(a.s, row, 1, 1, 0);
+      if (b < 0) continue;
+      const Kv8Seq q = kv8_sequence(a.s, b, capacity, t == 0 ? a.err : nullptr);
+      if (row - q.first >= q.n) continue;  // behind the last sequence, or not a valid one: left as it is
+      const int pos = q.pos0 + row - q.first;
+      __syncthreads();
+      for (int i = t; i < half; i += kKv8AppendThreads)
+        s_cs[0][i] = kv8_cos_sin(kv8_turns(__ldg(a.inv_freq + i)), pos, a.rope_scale);
+      __syncthreads();
+      const __half* src = a.qkv + row * row_elems;
+      __half* dst = a.q_out + static_cast<int64_t>(row) * a.Hq * kKv8D;
+      for (int v = t; v < a.Hq * 16; v += kKv8AppendThreads) {
+        float o[8];
+        kv8_rotated(src + (v >> 4) * kKv8D, v & 15, s_cs[0], a.rotary, a.interleaved, o);
+        uint4 pack;
+        __half2* h = reinterpret_cast<__half2*>(&pack);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(o[2 * j], o[2 * j + 1]);
+        reinterpret_cast<uint4*>(dst)[v] = pack;
+      }
+    }
+    return;
+  }
+  // item: a page that the call writes to. Sequence b's pages start at item
+  // start_b / P + 2 b: n new tokens touch at most n / P + 2 pages.
+  const int heads2 = 2 * a.c.Hkv;
+  const int64_t flat = static_cast<int64_t>(blockIdx.x) - a.q_blocks;
+  const int64_t item = flat / heads2;
+  const int kh = static_cast<int>(flat - item * heads2);  // K | V, head
+  int b, k;
+  if (a.s.q_start == nullptr) {
+    b = static_cast<int>(item);
+    k = 0;
+  } else {
+    b = kv8_find(a.s, item, 1, P, 2);
+    if (b < 0) return;
+    k = static_cast<int>(item - (kv8_row_start(a.s, b) / P + 2 * static_cast<int64_t>(b)));
+  }
+  const Kv8Seq q = kv8_sequence(a.s, b, capacity, t == 0 ? a.err : nullptr);
+  if (q.n <= 0) return;
+  const int page_no = q.pos0 / P + k;
+  if (page_no > (q.len - 1) / P) return;
+  const int base = page_no * P;                           // position of the page's first place
+  const int lo = max(q.pos0 - base, 0), hi = min(q.len - base, P);  // places [lo, hi) are new
+  const int page = __ldg(a.c.table + static_cast<int64_t>(b) * a.c.max_blocks + page_no);
+  if (page < 0 || page >= a.c.num_pages) {
+    if (t == 0) atomicCAS(a.err, 0, kErrKv8Range);
+    return;
+  }
+  const int64_t block = static_cast<int64_t>(page) * heads2 + kh;
+  int8_t* codes = a.c.codes + block * P * kKv8D;
+  const bool is_k = kh < a.c.Hkv;
+  const __half* src = a.qkv + (static_cast<int64_t>(q.first) + base - q.pos0) * row_elems +
+                      static_cast<int64_t>(a.Hq + kh) * kKv8D;  // place 0 of the page (read from place lo on)
+  const int i = t & 15;
+  float x[kPasses][8];
+  float amax = 0.0f;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int j = p * kSlab + (t >> 4);
+    if (is_k && (p + 1) * kSlab > lo && p * kSlab < hi) {  // the slab holds new tokens
+      __syncthreads();
+      for (int f = t & 15; f < half; f += 16)
+        s_cs[t >> 4][f] = kv8_cos_sin(kv8_turns(__ldg(a.inv_freq + f)), base + j, a.rope_scale);
+      __syncthreads();
+    }
+    if (j >= lo && j < hi) {
+      kv8_rotated(src + j * row_elems, i, s_cs[t >> 4], is_k ? a.rotary : 0, a.interleaved, x[p]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[p][e]));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float s_old = lo > 0 ? a.c.scales[block] : 0.0f;
+  if ((t & 31) == 0) s_red[t >> 5] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kKv8AppendThreads / 32; ++w) amax = fmaxf(amax, s_red[w]);
+  const float s_new = fmaxf(s_old, __fdiv_rn(amax, 127.0f));
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int j = p * kSlab + (t >> 4);
+    if (j >= lo && j < hi) {
+      uint32_t w[2] = {0u, 0u};
+      if (s_new > 0.0f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = max(-127, min(127, __float2int_rn(__fdiv_rn(x[p][e], s_new))));
+          w[e >> 2] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (e & 3));
+        }
+      }
+      *reinterpret_cast<uint2*>(codes + j * kKv8D + 8 * i) = make_uint2(w[0], w[1]);
+    }
+  }
+  if (lo > 0 && s_new > s_old) {  // the codes that were there, carried over to the larger scale
+    const float ratio = __fdiv_rn(s_old, s_new);
+    for (int v = t; v < lo * 16; v += kKv8AppendThreads) {
+      uint2* at = reinterpret_cast<uint2*>(codes) + v;
+      const uint2 c = *at;
+      uint32_t w[2] = {c.x, c.y}, u[2] = {0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int old = static_cast<int8_t>(w[e >> 2] >> (8 * (e & 3)));
+        u[e >> 2] |= (static_cast<uint32_t>(__float2int_rn(static_cast<float>(old) * ratio)) & 0xFFu) << (8 * (e & 3));
+      }
+      *at = make_uint2(u[0], u[1]);
+    }
+  }
+  if (t == 0) a.c.scales[block] = s_new;
+}
+
+}  // namespace w4a8

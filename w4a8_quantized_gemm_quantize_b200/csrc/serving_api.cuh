@@ -1,0 +1,172 @@
+// C ABI of the serving operators around the GEMMs: the norm that quantizes,
+// and the paged 8-bit KV cache with its append and attention. Declarations
+// and contracts in include/w4a8.h; the helpers are w4a8_api.cu's.
+#pragma once
+#include "kv8_attention.cuh"
+#include "rmsnorm_quantize.cuh"
+
+namespace w4a8 {
+namespace {
+
+constexpr int64_t kKv8MaxLen = int64_t(1) << 24;
+
+template <int THREADS, int VPT>
+w4a8_status_t launch_rmsnorm(const __half* X, const __half* R, const __half* W, float eps, int64_t M, int64_t K,
+                             __half* H, int8_t* A8, __half* sA, int32_t* rowsum, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(M));
+  const int early = M <= kEarlyReleaseRows ? 1 : 0;
+  if (R != nullptr)
+    return launch_pdl(rmsnorm_quantize_kernel<THREADS, VPT, true>, grid, dim3(THREADS), 0, st, 1, X, R, W, eps, K, H,
+                      A8, sA, rowsum, early);
+  return launch_pdl(rmsnorm_quantize_kernel<THREADS, VPT, false>, grid, dim3(THREADS), 0, st, 1, X, R, W, eps, K, H,
+                    A8, sA, rowsum, early);
+}
+
+// Checks of a cache descriptor and of the batch's sizes. max_table: entries
+// the table is indexed with stay below 2^31 per sequence.
+w4a8_status_t check_kv8(const w4a8_kv8_cache_t* c, int64_t B, int64_t T, int64_t Hq) {
+  if (c == nullptr) return W4A8_ERR_INVALID_ARG;
+  if (c->reserved != 0 || B < 0 || T < 0 || Hq < 0 || c->num_pages < 0 || c->max_blocks < 0 || c->Hkv < 0)
+    return W4A8_ERR_INVALID_ARG;
+  if (c->D != kKv8D || !(c->page == 16 || c->page == 32 || c->page == 64 || c->page == 128))
+    return W4A8_ERR_UNSUPPORTED_SHAPE;
+  if (c->Hkv == 0 || Hq == 0 || Hq % c->Hkv != 0 || Hq > 1024 || c->num_pages == 0 || c->max_blocks == 0 ||
+      c->max_blocks * c->page > kKv8MaxLen || c->num_pages * 2 * c->Hkv > INT32_MAX / c->page || B > 65535 ||
+      T > INT32_MAX / 1024)
+    return W4A8_ERR_UNSUPPORTED_SHAPE;
+  return W4A8_OK;
+}
+
+w4a8_status_t check_kv8_pointers(const w4a8_kv8_cache_t* c, const int32_t* seq_lens, const int32_t* q_start) {
+  if (c->codes == nullptr || c->scales == nullptr || c->block_table == nullptr || seq_lens == nullptr)
+    return W4A8_ERR_INVALID_ARG;
+  if (!aligned(c->codes, 128) || !aligned(c->scales, 4) || !aligned(c->block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(q_start, 4))
+    return W4A8_ERR_MISALIGNED;
+  return W4A8_OK;
+}
+
+Kv8Cache kv8_cache_args(const w4a8_kv8_cache_t* c) {
+  return {c->codes, c->scales, c->block_table, static_cast<int>(c->num_pages), static_cast<int>(c->max_blocks),
+          c->Hkv, c->page};
+}
+
+w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int32_t* seq_lens, const int32_t* q_start,
+                            int64_t B, int64_t T, int64_t Hq, float scale, void* out, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
+  w4a8_status_t st = check_kv8(c, B, T, Hq);
+  if (st != W4A8_OK || B == 0 || T == 0) return st;
+  st = check_kv8_pointers(c, seq_lens, q_start);
+  if (st != W4A8_OK) return st;
+  if (q == nullptr || out == nullptr) return W4A8_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return W4A8_ERR_MISALIGNED;
+  if (workspace == nullptr || workspace_bytes < w4a8_kv8_attention_workspace_bytes(B, T, Hq, c->Hkv))
+    return W4A8_ERR_WORKSPACE;
+  DeviceInfo* dev = nullptr;
+  st = device_info(&dev);
+  if (st != W4A8_OK) return st;
+  Kv8AttnArgs a;
+  a.q = static_cast<const __half*>(q);
+  a.c = kv8_cache_args(c);
+  a.s = {seq_lens, q_start, static_cast<int>(B), static_cast<int>(T)};
+  a.out = static_cast<__half*>(out);
+  a.Hq = static_cast<int>(Hq);
+  a.scale = scale;
+  a.err = dev->err;
+  const int64_t blocks = (T * Hq + kKv8SimpleWarps - 1) / kKv8SimpleWarps;
+  return launch_pdl(kv8_attention_simple_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kKv8SimpleWarps * 32), 0,
+                    stream, 1, a);
+}
+
+}  // namespace
+}  // namespace w4a8
+
+extern "C" {
+
+w4a8_status_t w4a8_rmsnorm_quantize_act(const void* X, const void* residual, const void* weight, float eps, int64_t M,
+                                        int64_t K, void* H, int8_t* A8, void* sA, int32_t* rowsum,
+                                        w4a8_stream_t stream) {
+  const w4a8_status_t st = check_quantize_args(X, M, K, A8, sA, rowsum);
+  if (st != W4A8_OK || M == 0) return st;
+  if (weight == nullptr || (residual == nullptr) != (H == nullptr) || !(eps >= 0.0f)) return W4A8_ERR_INVALID_ARG;
+  if (!aligned(weight, 16) || !aligned(residual, 16) || !aligned(H, 16)) return W4A8_ERR_MISALIGNED;
+  const __half* x = static_cast<const __half*>(X);
+  const __half* r = static_cast<const __half*>(residual);
+  const __half* w = static_cast<const __half*>(weight);
+  __half* h = static_cast<__half*>(H);
+  __half* s = static_cast<__half*>(sA);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t nvec = K / 8;
+  if (nvec <= 128) return launch_rmsnorm<128, 1>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
+  if (nvec <= 256) return launch_rmsnorm<256, 1>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
+  if (nvec <= 512) return launch_rmsnorm<256, 2>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
+  if (nvec <= 1024) return launch_rmsnorm<256, 4>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
+  if (nvec <= 2048) return launch_rmsnorm<512, 4>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
+  if (nvec <= 4096) return launch_rmsnorm<1024, 4>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
+  return launch_rmsnorm<1024, 8>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
+}
+
+w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cache_t* cache, const int32_t* seq_lens,
+                                   const int32_t* q_start, int64_t B, int64_t T, int64_t Hq, const float* inv_freq,
+                                   int32_t rotary_dim, int32_t interleaved, float rope_scale, void* q_out,
+                                   w4a8_stream_t stream) {
+  w4a8_status_t st = check_kv8(cache, B, T, Hq);
+  if (st != W4A8_OK) return st;
+  if (interleaved != 0 && interleaved != 1) return W4A8_ERR_INVALID_ARG;
+  if (rotary_dim < 0 || rotary_dim > kKv8D || rotary_dim % 2 != 0) return W4A8_ERR_UNSUPPORTED_SHAPE;
+  if (B == 0 || T == 0) return W4A8_OK;
+  if (q_start == nullptr && B != T) return W4A8_ERR_INVALID_ARG;
+  st = check_kv8_pointers(cache, seq_lens, q_start);
+  if (st != W4A8_OK) return st;
+  if (qkv == nullptr || q_out == nullptr || (rotary_dim > 0 && inv_freq == nullptr)) return W4A8_ERR_INVALID_ARG;
+  if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(inv_freq, 4)) return W4A8_ERR_MISALIGNED;
+  DeviceInfo* dev = nullptr;
+  st = device_info(&dev);
+  if (st != W4A8_OK) return st;
+  Kv8AppendArgs a;
+  a.qkv = static_cast<const __half*>(qkv);
+  a.c = kv8_cache_args(cache);
+  a.s = {seq_lens, q_start, static_cast<int>(B), static_cast<int>(T)};
+  a.inv_freq = inv_freq;
+  a.q_out = static_cast<__half*>(q_out);
+  a.Hq = static_cast<int>(Hq);
+  a.rotary = rotary_dim;
+  a.interleaved = interleaved;
+  a.rope_scale = rope_scale;
+  a.err = dev->err;
+  a.q_rows = T > 8 * dev->sms ? 4 : 1;
+  a.q_blocks = static_cast<int>((T + a.q_rows - 1) / a.q_rows);
+  const int64_t items = q_start == nullptr ? B : T / cache->page + 2 * B;
+  const int64_t grid = a.q_blocks + items * 2 * cache->Hkv;
+  if (grid > INT32_MAX) return W4A8_ERR_UNSUPPORTED_SHAPE;
+  const dim3 g(static_cast<unsigned>(grid)), block(kKv8AppendThreads);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  switch (cache->page) {
+    case 16: return launch_pdl(kv8_append_kernel<16>, g, block, 0, cs, 1, a);
+    case 32: return launch_pdl(kv8_append_kernel<32>, g, block, 0, cs, 1, a);
+    case 64: return launch_pdl(kv8_append_kernel<64>, g, block, 0, cs, 1, a);
+    default: return launch_pdl(kv8_append_kernel<128>, g, block, 0, cs, 1, a);
+  }
+}
+
+size_t w4a8_kv8_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
+  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
+  return 256;
+}
+
+w4a8_status_t w4a8_kv8_attention_decode(const void* q, const w4a8_kv8_cache_t* cache, const int32_t* seq_lens,
+                                        int64_t B, int64_t Hq, float scale, void* out, void* workspace,
+                                        size_t workspace_bytes, w4a8_stream_t stream) {
+  return kv8_attention(q, cache, seq_lens, nullptr, B, B, Hq, scale, out, workspace, workspace_bytes,
+                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+w4a8_status_t w4a8_kv8_attention_prefill(const void* q, const w4a8_kv8_cache_t* cache, const int32_t* seq_lens,
+                                         const int32_t* q_start, int64_t B, int64_t T, int64_t Hq, float scale,
+                                         void* out, void* workspace, size_t workspace_bytes, w4a8_stream_t stream) {
+  if (q_start == nullptr && B > 0 && T > 0) return W4A8_ERR_INVALID_ARG;
+  return kv8_attention(q, cache, seq_lens, q_start, B, T, Hq, scale, out, workspace, workspace_bytes,
+                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
