@@ -51,6 +51,57 @@ Kv8Cache kv8_cache_args(const w4a8_kv8_cache_t* c) {
           c->Hkv, c->page};
 }
 
+// The cache's codes as rows of 128 bytes, loaded in boxes of a decode tile's
+// rows (a page's, where that is smaller) with the 128-byte swizzle.
+w4a8_status_t kv8_map(const w4a8_kv8_cache_t* c, int box_rows, CUtensorMap* map) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kKv8D),
+                              static_cast<cuuint64_t>(c->num_pages) * 2 * c->Hkv * c->page};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kKv8D)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kKv8D),
+                             static_cast<cuuint32_t>(c->page < box_rows ? c->page : box_rows)};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c->codes, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? W4A8_OK
+             : W4A8_ERR_CUDA;
+}
+
+template <bool DUP>
+w4a8_status_t launch_kv8_decode(const CUtensorMap& map, const Kv8DecodeArgs& d, int grid, cudaStream_t stream) {
+  static bool done[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return launch_status();
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(kv8_decode_kernel<DUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecSmem::kBytes) !=
+        cudaSuccess)
+      return launch_status();
+    done[dev] = true;
+  }
+  return launch_pdl(kv8_decode_kernel<DUP>, dim3(static_cast<unsigned>(grid)), dim3(kDecWarps * 32), DecSmem::kBytes,
+                    stream, 1, map, d);
+}
+
+w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_cache_t* c, void* workspace,
+                         cudaStream_t stream) {
+  CUtensorMap map;
+  const w4a8_status_t st = kv8_map(c, kDecTile, &map);
+  if (st != W4A8_OK) return st;
+  const int G = a.Hq / a.c.Hkv;
+  Kv8DecodeArgs d;
+  d.a = a;
+  d.count = static_cast<int*>(workspace);
+  d.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kDecMaxCtas * 4);
+  d.groups = (G + kDecCols - 1) / kDecCols;
+  // one CTA per SM, no more than the longest possible batch has tiles for
+  const int64_t tiles = (c->max_blocks * c->page + kDecTile - 1) / kDecTile * a.s.B * a.c.Hkv * d.groups;
+  int64_t grid = (tiles + kDecWarps - 1) / kDecWarps;
+  if (grid > dev->sms) grid = dev->sms;
+  if (grid > kDecMaxCtas) grid = kDecMaxCtas;
+  if (G <= 4) return launch_kv8_decode<true>(map, d, static_cast<int>(grid), stream);
+  return launch_kv8_decode<false>(map, d, static_cast<int>(grid), stream);
+}
+
 w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int32_t* seq_lens, const int32_t* q_start,
                             int64_t B, int64_t T, int64_t Hq, float scale, void* out, void* workspace,
                             size_t workspace_bytes, cudaStream_t stream) {
@@ -73,6 +124,7 @@ w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int3
   a.Hq = static_cast<int>(Hq);
   a.scale = scale;
   a.err = dev->err;
+  if (q_start == nullptr) return kv8_decode(a, dev, c, workspace, stream);
   const int64_t blocks = (T * Hq + kKv8SimpleWarps - 1) / kKv8SimpleWarps;
   return launch_pdl(kv8_attention_simple_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kKv8SimpleWarps * 32), 0,
                     stream, 1, a);
@@ -151,7 +203,7 @@ w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cache_t* cach
 
 size_t w4a8_kv8_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
   if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
-  return 256;
+  return kDecMaxCtas * (4 + 2 * kDecPart * sizeof(float));
 }
 
 w4a8_status_t w4a8_kv8_attention_decode(const void* q, const w4a8_kv8_cache_t* cache, const int32_t* seq_lens,
