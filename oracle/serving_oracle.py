@@ -99,11 +99,12 @@ def gather(codes, scales, table, b, L, g):
     return v.transpose(1, 0, 2, 3).reshape(2, -1, D)[:, :L]
 
 
-def attention(q, codes, scales, table, seq_lens, q_start, scale, weight_eps=0.0, heads=None):
+def attention(q, codes, scales, table, seq_lens, q_start, scale, weight_eps=0.0, heads=None, weight_floor=0.0):
     """(y, E) float64 [T, Hq, 128]: the exact outputs and a bound on what an
     fp32 evaluation in any order and split may be off by, with the softmax
-    weights of the numerator rounded to `weight_eps` relative. Rows of no
-    sequence are NaN. u = 2^-23:
+    weights of the numerator rounded to `weight_eps` relative, or, where that
+    is more, by `weight_floor` of the row's largest weight. Rows of no sequence
+    are NaN. u = 2^-23:
 
     * a score: products exact (11-bit by 8-bit significands), their 128-term sum
       gamma_128 sum |q c|, three rounded factors: delta_j = scale * sK * gamma_131
@@ -130,6 +131,8 @@ def attention(q, codes, scales, table, seq_lens, q_start, scale, weight_eps=0.0,
             K, V = gather(codes, scales, table, b, L, h // (Hq // Hkv))
             sv = np.repeat(scales[np.asarray(table[b, :-(-L // codes.shape[3])], np.int64), 1, h // (Hq // Hkv)],
                            codes.shape[3])[:L].astype(np.float64)
+            rows = np.asarray(table[b, :-(-L // codes.shape[3])], np.int64)
+            C = np.abs(codes[rows, 1, h // (Hq // Hkv)].reshape(-1, D)[:L].astype(np.float64))
             for i in range(n):
                 m = pos0 + i + 1
                 s = scale * (K[:m] @ q[first + i, h])
@@ -141,5 +144,7 @@ def attention(q, codes, scales, table, seq_lens, q_start, scale, weight_eps=0.0,
                 R = np.expm1(2 * d.max() + 8 * U * (np.abs(s - s.max()) + lg) + 16 * U)
                 a = (p @ np.abs(V[:m])) / p.sum()
                 e = (p * R) @ np.abs(V[:m] - o) / (p * (1 - np.minimum(R, 0.5))).sum() + weight_eps * a
+                if weight_floor:
+                    e = e + weight_floor * (p * sv[:m]).max() * C[:m].sum(axis=0) / p.sum()
                 E[first + i, h] = 1.1 * (e + (2 * m + 64) * U * (a + np.abs(o)))
     return y, E

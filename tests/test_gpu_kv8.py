@@ -6,8 +6,12 @@ sine and cosine by 2^-22, so a rotated value by 2^-20 of its pair's larger
 half (ROT), scale factor included; a page's scale is within 2 ROT of the
 exact one relatively; with the scale taken as given a new code is within 1/2
 + 127 * 4 ROT of x / s', a carried code within 1/2 + 127 * 2^-22. Attention:
-oracle.attention's bound plus half an fp16 ulp; the decode kernels keep the
+the oracle's bound plus half an fp16 ulp; the decode kernels keep the
 softmax weights to 2^-20, the prefill kernel rounds them to fp16 (2^-11).
+Both hold them in fp16 with the largest at 2^14 (decode, two terms) or at
+least 2^10 (prefill), where the smallest step is 2^-24: a rounding there is
+off by 2^-25, i.e. by 2^-39 or 2^-35 of the largest weight, however small the
+weight itself (the floor of the bound).
 """
 import numpy as np
 import pytest
@@ -196,7 +200,7 @@ def attend(c, decode, ws=None):
 
 
 def check_attention(c, y, weight_eps, heads=None):
-    o, E = S.attention(*c, SCALE, weight_eps, heads)
+    o, E = S.attention(*c, SCALE, weight_eps, heads, 2.0 ** -39 if weight_eps < 2.0 ** -12 else 2.0 ** -35)
     n = int(c[-1][-1])
     hs = slice(None) if heads is None else list(heads)
     o, E, got = o[:n, hs], E[:n, hs], y[:n, hs].astype(np.float64)

@@ -2,7 +2,7 @@
 // and the paged 8-bit KV cache with its append and attention. Declarations
 // and contracts in include/w4a8.h; the helpers are w4a8_api.cu's.
 #pragma once
-#include "kv8_attention.cuh"
+#include "kv8_prefill.cuh"
 #include "rmsnorm_quantize.cuh"
 
 namespace w4a8 {
@@ -102,6 +102,23 @@ w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_c
   return launch_kv8_decode<false>(map, d, static_cast<int>(grid), stream);
 }
 
+w4a8_status_t kv8_prefill(const Kv8AttnArgs& a, const w4a8_kv8_cache_t* c, cudaStream_t stream) {
+  static bool done[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return launch_status();
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(kv8_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PreSmem::kBytes) !=
+        cudaSuccess)
+      return launch_status();
+    done[dev] = true;
+  }
+  // slots of 256 rows: sequence b's begin at start_b G / 256 + b
+  const int64_t slots = static_cast<int64_t>(a.s.T) * (a.Hq / a.c.Hkv) / (2 * kPreRows) + a.s.B;
+  if (slots * a.c.Hkv > INT32_MAX) return W4A8_ERR_UNSUPPORTED_SHAPE;
+  return launch_pdl(kv8_prefill_kernel, dim3(static_cast<unsigned>(slots * a.c.Hkv)), dim3(kPreThreads),
+                    PreSmem::kBytes, stream, 1, a, static_cast<int>(slots));
+}
+
 w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int32_t* seq_lens, const int32_t* q_start,
                             int64_t B, int64_t T, int64_t Hq, float scale, void* out, void* workspace,
                             size_t workspace_bytes, cudaStream_t stream) {
@@ -125,9 +142,7 @@ w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int3
   a.scale = scale;
   a.err = dev->err;
   if (q_start == nullptr) return kv8_decode(a, dev, c, workspace, stream);
-  const int64_t blocks = (T * Hq + kKv8SimpleWarps - 1) / kKv8SimpleWarps;
-  return launch_pdl(kv8_attention_simple_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kKv8SimpleWarps * 32), 0,
-                    stream, 1, a);
+  return kv8_prefill(a, c, stream);
 }
 
 }  // namespace
