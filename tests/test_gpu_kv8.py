@@ -311,6 +311,19 @@ def test_prefill_many_sequences():
     check_attention(c, attend(c, False), 2.0 ** -11)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (32, 8), (6, 6), (12, 1)])
+def test_prefill_few_and_many_rows_together(Hq, Hkv):
+    """Sequences of a few rows beside long chunks, ragged limits that end a tile early, padding rows behind."""
+    c = case(Hq, Hkv, 32, [1, 300, 8, 2, 0, 9, 33, 5], [500, 70, 0, 31, 7, 1000, 95, 3000], 400 + Hq, pad_rows=5)
+    check_attention(c, attend(c, False), 2.0 ** -11)
+
+
+def test_prefill_one_sequence_with_padding_rows():
+    """More rows in the batch than the one sequence has."""
+    c = case(4, 1, 16, [3], [50], 24, pad_rows=200)
+    check_attention(c, attend(c, False), 2.0 ** -11)
+
+
 def test_prefill_of_single_tokens_is_decode():
     c = case(8, 2, 64, [1] * 6, [0, 64, 700, 5, 63, 200], 23)
     check_attention(c, attend(c, False), 2.0 ** -11)

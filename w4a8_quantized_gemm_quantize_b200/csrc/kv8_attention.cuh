@@ -89,7 +89,12 @@ __device__ __forceinline__ void kv8_wait(uint64_t* bar, uint32_t parity, DevErr 
 // / sV_j in fp32. Up to four heads share the 8 columns as hi (0-3) and lo
 // (4-7); up to eight take a second product for lo.
 //
-// Work is dealt out by tiles: all (sequence, kv head, head group) pairs' tiles
+// The 8 columns are rows of a kv head's query group: row R = i G + h is head h
+// at new token i, so that a handful of new tokens per sequence (a decode step's
+// one, guesses to be checked) take the same path, each column with its own
+// causal limit, more than 8 rows as further column groups.
+//
+// Work is dealt out by tiles: all (sequence, kv head, column group) pairs' tiles
 // in one line, cut evenly over the CTAs and over their warps. What a warp
 // finishes alone it writes; partial results of a pair meet in shared memory,
 // then, where a pair crosses CTAs, in the workspace, where the last CTA to
@@ -109,7 +114,7 @@ constexpr int kDecMaxCtas = 256;
 struct DecSmem {
   static constexpr int kOffPart = kDecWarps * kDecRingBytes;
   static constexpr int kOffPairs = kOffPart + kDecWarps * kDecPart * 4;
-  static constexpr int kOffBars = kOffPairs + kDecWarps * 2 * 24;
+  static constexpr int kOffBars = kOffPairs + kDecWarps * 2 * 32;
   static constexpr int kOffMeta = kOffBars + kDecWarps * kDecStages * 8;
   static constexpr int kOffLast = kOffMeta + kDecWarps * kDecStages * 16;
   static constexpr int kBytes = kOffLast + 16 + 1024;  // + alignment slack
@@ -121,24 +126,35 @@ struct Kv8DecodeArgs {
   Kv8AttnArgs a;
   int* count;   // [gridDim.x] arrivals of pairs that cross CTAs, zero between calls
   float* part;  // [gridDim.x][2][kDecPart]
-  int groups;   // head groups of up to 8 query heads per kv head
+  int max_rows; // sequences with more rows (new tokens times G) are another kernel's
 };
 
 // One pair's place in the line of tiles.
 struct DecPair {
-  int b, j;        // sequence (-1: none), (kv head, head group) within it
+  int b, j;        // sequence (-1: none), (kv head, column group) within it
   int len, tiles;  // cached tokens, tiles of each of the sequence's pairs
+  int row0, n;     // its first row of the batch, its new tokens
   int64_t first;   // the pair's first tile in the line
 };
-static_assert(sizeof(DecPair) == 24, "DecSmem");
+static_assert(sizeof(DecPair) == 32, "DecSmem");
 
-__device__ __forceinline__ int dec_len(const Kv8AttnArgs& a, int b, int64_t capacity, bool report) {
-  const int len = __ldg(a.s.seq_lens + b);
-  if (len >= 0 && len <= capacity) return len;
-  if (report) atomicCAS(a.err, 0, kErrKv8Range);
-  return len < 0 ? 0 : static_cast<int>(capacity);
+// Sequence b's lengths; tiles == 0: it has no part in this kernel's work.
+__device__ __forceinline__ DecPair dec_sequence(const Kv8AttnArgs& a, int b, int G, int max_rows, bool report) {
+  DecPair p = {b, 0, 0, 0, 0, 0, 0};
+  if (b >= a.s.B) return p;
+  const int64_t capacity = static_cast<int64_t>(a.c.max_blocks) * a.c.P;
+  p.row0 = kv8_row_start(a.s, b);
+  p.n = a.s.q_start == nullptr ? 1 : kv8_row_start(a.s, b + 1) - p.row0;
+  if (p.n <= 0 || static_cast<int64_t>(p.n) * G > max_rows) return p;
+  p.len = __ldg(a.s.seq_lens + b);
+  const int least = a.s.q_start == nullptr ? 0 : p.n;
+  if (p.len < least || p.len > capacity) {
+    if (report) atomicCAS(a.err, 0, kErrKv8Range);
+    p.len = a.s.q_start == nullptr && p.len > 0 ? static_cast<int>(capacity) : 0;
+  }
+  p.tiles = p.len > 0 ? (p.len + kDecTile - 1) / kDecTile : 1;
+  return p;
 }
-__device__ __forceinline__ int dec_tiles(int len) { return len > 0 ? (len + kDecTile - 1) / kDecTile : 1; }
 
 // Adds partial result (m2, l2, o2) to (m, l, o), m in powers of two.
 __device__ __forceinline__ void dec_join(float& m, float& l, float4& o, float m2, float l2, float4 o2) {
@@ -155,6 +171,11 @@ __device__ __forceinline__ uint2 dec_pack(float4 o, float l) {
   const float r = l > 0.0f ? 1.0f / l : 0.0f;
   const __half2 a = __floats2half2_rn(o.x * r, o.y * r), b = __floats2half2_rn(o.z * r, o.w * r);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// Where row R of a sequence's kv head lies in q and out.
+__device__ __forceinline__ int64_t dec_row(const Kv8AttnArgs& a, const DecPair& p, int G, int kvh, int R) {
+  return ((static_cast<int64_t>(p.row0) + R / G) * a.Hq + kvh * G + R % G) * kKv8D;
 }
 
 template <bool DUP>
@@ -174,8 +195,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
                                               : sm + DecSmem::kOffPart + (entry >> 1) * kDecPart * 4);
   };
   const DevErr err{a.err};
-  const int P = a.c.P, G = a.Hq / a.c.Hkv, NP = a.c.Hkv * args.groups;
-  const int64_t capacity = static_cast<int64_t>(a.c.max_blocks) * P;
+  const int P = a.c.P, G = a.Hq / a.c.Hkv;
+  const auto groups_of = [&](int n) { return (n * G + kDecCols - 1) / kDecCols; };
   if (lane < kDecStages) mbar_init(bars + lane, 5);  // the bulk copies, and four scales
   fence_barrier_init();
   __syncwarp();
@@ -184,10 +205,12 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
 
   // the line's length, and this CTA's and this warp's part of it
   int64_t total = 0;
-  for (int b = lane; b < a.s.B; b += 32)
-    total += dec_tiles(dec_len(a, b, capacity, blockIdx.x == 0 && warp == 0));
+  for (int b = lane; b < a.s.B; b += 32) {
+    const DecPair p = dec_sequence(a, b, G, args.max_rows, blockIdx.x == 0 && warp == 0);
+    total += static_cast<int64_t>(p.tiles) * groups_of(p.n) * a.c.Hkv;
+  }
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= NP;
+  if (total == 0) return;
   const int64_t want = (total + kDecWarps - 1) / kDecWarps;
   const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
   if (static_cast<int>(blockIdx.x) >= ctas) return;
@@ -198,10 +221,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
   // the pair that holds tile x of the line
   const auto locate = [&](int64_t x) {
     int64_t base = 0;
-    DecPair p = {0, 0, 0, 1, 0};
+    DecPair p = {0, 0, 0, 1, 0, 0, 0};
     for (int b0 = 0; b0 < a.s.B; b0 += 32) {
-      const int len = b0 + lane < a.s.B ? dec_len(a, b0 + lane, capacity, false) : 0;
-      const int n = b0 + lane < a.s.B ? dec_tiles(len) * NP : 0;
+      const DecPair q = dec_sequence(a, b0 + lane, G, args.max_rows, false);
+      const int64_t n = static_cast<int64_t>(q.tiles) * groups_of(q.n) * a.c.Hkv;
       int64_t sum = n;
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
@@ -211,8 +234,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
       if (in != 0) {
         const int src = __ffs(in) - 1;
         p.b = b0 + src;
-        p.len = __shfl_sync(0xffffffffu, len, src);
-        p.tiles = dec_tiles(p.len);
+        p.len = __shfl_sync(0xffffffffu, q.len, src);
+        p.tiles = __shfl_sync(0xffffffffu, q.tiles, src);
+        p.row0 = __shfl_sync(0xffffffffu, q.row0, src);
+        p.n = __shfl_sync(0xffffffffu, q.n, src);
         const int64_t first = base + __shfl_sync(0xffffffffu, sum - n, src);
         p.j = static_cast<int>((x - first) / p.tiles);
         p.first = first + static_cast<int64_t>(p.j) * p.tiles;
@@ -223,13 +248,13 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     return p;
   };
   const auto advance = [&](DecPair& p) {  // to the next pair of the line
-    p.first += p.tiles;
-    if (++p.j == NP) {
-      p.j = 0;
-      ++p.b;
-      p.len = p.b < a.s.B ? dec_len(a, p.b, capacity, false) : 0;
-      p.tiles = dec_tiles(p.len);
+    const int64_t next = p.first + p.tiles;
+    if (++p.j == groups_of(p.n) * a.c.Hkv) {
+      int b = p.b;
+      do p = dec_sequence(a, ++b, G, args.max_rows, false);
+      while (p.tiles == 0 && b < a.s.B);
     }
+    p.first = next;
   };
 
   const int n_mine = static_cast<int>(we - ws);
@@ -261,7 +286,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     const int copies = n > 0 ? (n + rows_per_copy - 1) / rows_per_copy : 0;
     const int page0 = __shfl_sync(0xffffffffu, blk, b0 - blk0);
     const int page1 = __shfl_sync(0xffffffffu, blk, min(b0 - blk0 + blocks_per_tile - 1, 31));
-    const int kvh = nxt.j / args.groups;
+    const int kvh = nxt.j / groups_of(nxt.n);
     // lanes 0, 1: the scales of K (first, second half of the tile), 2, 3: of V
     if (lane < 4) {
       const int page = (lane & 1) && copies == 2 ? page1 : page0;
@@ -285,6 +310,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
 
   uint32_t qf[16];             // this lane's column's query, dimensions 32c ..
   float O[8][4], m[2], l[2];   // columns 2c, 2c + 1
+  int limit[2];                // tokens that they see
   bool fresh = true;
   int stage = 0;
   uint32_t phase = 0;
@@ -292,15 +318,20 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
   if (lane < 2) s_pairs[2 * warp + lane].b = -1;
   for (int it = 0; it < n_mine; ++it, ++x) {
     while (x >= cur.first + cur.tiles) advance(cur);
-    const int kvh = cur.j / args.groups, h0 = kvh * G + (cur.j % args.groups) * kDecCols;
-    const int nh = min(G - (cur.j % args.groups) * kDecCols, kDecCols);
     if (fresh) {
+      const int groups = groups_of(cur.n), r0 = cur.j % groups * kDecCols;
       const int col = DUP ? g & 3 : g;
+      const bool any = r0 + col < cur.n * G;
       const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (static_cast<int64_t>(cur.b) * a.Hq + h0 + min(col, nh - 1)) * kKv8D + 32 * c);
+          a.q + dec_row(a, cur, G, cur.j / groups, any ? r0 + col : 0) + 32 * c);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // (a column without a row: any limit from 1)
+        const int r = r0 + (DUP ? (2 * c + k) & 3 : 2 * c + k);
+        limit[k] = min(cur.len - cur.n + 1 + r / G, cur.len);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 v = col < nh ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = any ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
         qf[4 * i] = v.x;
         qf[4 * i + 1] = v.y;
         qf[4 * i + 2] = v.z;
@@ -356,7 +387,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int tok = mt * 16 + (k >> 1) * 8 + g;
-          S[mt][k] = tok < n ? S[mt][k] * sks[mt] + lsv[mt] : -INFINITY;
+          S[mt][k] = tok0 + tok < limit[k & 1] ? S[mt][k] * sks[mt] + lsv[mt] : -INFINITY;
           mx[k & 1] = fmaxf(mx[k & 1], S[mt][k]);
         }
 #pragma unroll
@@ -365,7 +396,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
         mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
       }
       if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
-        const float f[2] = {ex2(m[0] - mx[0]), ex2(m[1] - mx[1])};
+        const float f[2] = {mx[0] == m[0] ? 1.0f : ex2(m[0] - mx[0]), mx[1] == m[1] ? 1.0f : ex2(m[1] - mx[1])};
         m[0] = mx[0];
         m[1] = mx[1];
         l[0] *= f[0];
@@ -375,13 +406,15 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) O[i][k] *= f[k & 1];
       }
+      // (a column may have seen nothing yet: its tiles before this one are other warps')
+      const float up[2] = {m[0] == -INFINITY ? 0.0f : 14.0f - m[0], m[1] == -INFINITY ? 0.0f : 14.0f - m[1]};
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         const float isv = ex2(-lsv[mt]);
         float w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          w[k] = ex2(S[mt][k] - m[k & 1] + 14.0f);
+          w[k] = ex2(S[mt][k] + up[k & 1]);
           l[k & 1] += w[k] * isv;
         }
         uint32_t bh[2], bl[2];
@@ -445,11 +478,12 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     const bool whole = cur.first >= ws && cur.first + cur.tiles <= we;
     const int slot = cur.first <= ws ? 0 : 1;
     if (whole) {
+      const int groups = groups_of(cur.n), r0 = cur.j % groups * kDecCols;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int col = 2 * c + k;
-        if (col < nh && (!DUP || c < 2)) {
-          __half* dst = a.out + (static_cast<int64_t>(cur.b) * a.Hq + h0 + col) * kKv8D + 16 * g;
+        if (r0 + col < cur.n * G && (!DUP || c < 2)) {
+          __half* dst = a.out + dec_row(a, cur, G, cur.j / groups, r0 + col) + 16 * g;
           const float r = l[k] > 0.0f ? 1.0f / l[k] : 0.0f;
           uint4 y[2];
           __half2* hv = reinterpret_cast<__half2*>(y);
@@ -479,15 +513,15 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
   __syncthreads();
 
   // ---- partial results of one pair, joined in the order of the line: warp w
-  // takes query head w of the group, lane l dimensions 4l .. 4l + 3
+  // takes column w, lane l dimensions 4l .. 4l + 3
   for (int e = 0; e < 2 * kDecWarps;) {
     const DecPair p = s_pairs[e];
     if (p.b < 0) {
       ++e;
       continue;
     }
-    const int kvh = p.j / args.groups, h0 = kvh * G + (p.j % args.groups) * kDecCols;
-    const int nh = min(G - (p.j % args.groups) * kDecCols, kDecCols);
+    const int groups = groups_of(p.n), r0 = p.j % groups * kDecCols;
+    const int nh = min(p.n * G - r0, kDecCols);
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (; e < 2 * kDecWarps; ++e) {
@@ -499,7 +533,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
                  reinterpret_cast<const float4*>(part + 2 * kDecCols + warp * kKv8D)[lane]);
       }
     }
-    uint2* dst = reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(p.b) * a.Hq + h0 + warp) * kKv8D) + lane;
+    uint2* dst = reinterpret_cast<uint2*>(a.out + dec_row(a, p, G, p.j / groups, r0 + min(warp, nh - 1))) + lane;
     if (p.first >= cs && p.first + p.tiles <= ce) {
       if (warp < nh) *dst = dec_pack(o, l);
       continue;

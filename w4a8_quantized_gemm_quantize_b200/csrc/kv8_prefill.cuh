@@ -72,7 +72,7 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[1
       : "memory");
 }
 
-__global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs a, int slots) {
+__global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs a, int slots, int few_rows) {
   extern __shared__ __align__(1024) uint8_t pre_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pre_smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + PreSmem::kOffBars);
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
   const int first = sq.first, n = kv8_row_start(a.s, b + 1) - first;
   const int64_t row0 = static_cast<int64_t>(slot - (static_cast<int64_t>(first) * G / (2 * kPreRows) + b)) * 2 * kPreRows;
   const int64_t rows = static_cast<int64_t>(n) * G;
-  if (row0 >= rows) return;
+  if (row0 >= rows || rows <= few_rows) return;  // (few rows: the decode kernel's)
   if (sq.n < 0) {  // a length that does not fit (reported): zeros
     const int64_t r = row0 + t;
     if (t < 2 * kPreRows && r < rows) {

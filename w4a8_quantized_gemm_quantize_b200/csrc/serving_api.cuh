@@ -82,6 +82,10 @@ w4a8_status_t launch_kv8_decode(const CUtensorMap& map, const Kv8DecodeArgs& d, 
                     stream, 1, map, d);
 }
 
+// Sequences whose rows (new tokens times query heads per kv head) are at most
+// this many go to the decode kernel, others to the prefill kernel.
+constexpr int kKv8FewRows = 32;
+
 w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_cache_t* c, void* workspace,
                          cudaStream_t stream) {
   CUtensorMap map;
@@ -92,17 +96,18 @@ w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_c
   d.a = a;
   d.count = static_cast<int*>(workspace);
   d.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kDecMaxCtas * 4);
-  d.groups = (G + kDecCols - 1) / kDecCols;
+  d.max_rows = a.s.q_start == nullptr ? G : kKv8FewRows;
   // one CTA per SM, no more than the longest possible batch has tiles for
-  const int64_t tiles = (c->max_blocks * c->page + kDecTile - 1) / kDecTile * a.s.B * a.c.Hkv * d.groups;
+  const int64_t tiles = (c->max_blocks * c->page + kDecTile - 1) / kDecTile * a.s.B * a.c.Hkv *
+                        ((d.max_rows + kDecCols - 1) / kDecCols);
   int64_t grid = (tiles + kDecWarps - 1) / kDecWarps;
   if (grid > dev->sms) grid = dev->sms;
   if (grid > kDecMaxCtas) grid = kDecMaxCtas;
-  if (G <= 4) return launch_kv8_decode<true>(map, d, static_cast<int>(grid), stream);
+  if (d.max_rows <= 4) return launch_kv8_decode<true>(map, d, static_cast<int>(grid), stream);
   return launch_kv8_decode<false>(map, d, static_cast<int>(grid), stream);
 }
 
-w4a8_status_t kv8_prefill(const Kv8AttnArgs& a, const w4a8_kv8_cache_t* c, cudaStream_t stream) {
+w4a8_status_t kv8_prefill(const Kv8AttnArgs& a, int few_rows, cudaStream_t stream) {
   static bool done[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return launch_status();
@@ -116,7 +121,7 @@ w4a8_status_t kv8_prefill(const Kv8AttnArgs& a, const w4a8_kv8_cache_t* c, cudaS
   const int64_t slots = static_cast<int64_t>(a.s.T) * (a.Hq / a.c.Hkv) / (2 * kPreRows) + a.s.B;
   if (slots * a.c.Hkv > INT32_MAX) return W4A8_ERR_UNSUPPORTED_SHAPE;
   return launch_pdl(kv8_prefill_kernel, dim3(static_cast<unsigned>(slots * a.c.Hkv)), dim3(kPreThreads),
-                    PreSmem::kBytes, stream, 1, a, static_cast<int>(slots));
+                    PreSmem::kBytes, stream, 1, a, static_cast<int>(slots), few_rows);
 }
 
 w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int32_t* seq_lens, const int32_t* q_start,
@@ -142,7 +147,13 @@ w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int3
   a.scale = scale;
   a.err = dev->err;
   if (q_start == nullptr) return kv8_decode(a, dev, c, workspace, stream);
-  return kv8_prefill(a, c, stream);
+  // each kernel takes the sequences that suit it; one whose share must be
+  // empty is not launched
+  const int64_t rows = T * (Hq / c->Hkv);
+  if (rows <= kKv8FewRows) return kv8_decode(a, dev, c, workspace, stream);
+  if (B == 1) return kv8_prefill(a, 0, stream);
+  st = kv8_decode(a, dev, c, workspace, stream);
+  return st != W4A8_OK ? st : kv8_prefill(a, kKv8FewRows, stream);
 }
 
 }  // namespace
