@@ -661,28 +661,38 @@ def chain(links, workspace):
 
 
 # ------------------------------------------- between the GEMMs of a decoder layer
-# These run once or more per layer and step, so their host side is kept short:
-# plain integers for pointers, and the device is switched only when it differs.
-def _check_tensor(t, name, dtype, device, shape=None):
-    """One argument: CUDA, contiguous, of this type, device and shape (None in a shape: any)."""
+# These run once or more per layer and step, so their host side is kept short
+# (6 to 8 us a call, half of it the launch): plain integers for pointers, the
+# stream's handle without a Stream object, the device switched only when it
+# differs, and a message put together only for an argument that is refused.
+def _check_tensor(t, name, dtype, index, shape=None):
+    """One argument: contiguous, of this type and shape (None: any), on CUDA device `index`."""
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous() and (shape is None or t.shape == shape):
+        return
     if not t.is_cuda:
         raise W4A8Error("tensors must live on a CUDA device (no CPU path exists)")
     if not t.is_contiguous():
         raise W4A8Error("tensors must be contiguous")
-    if t.dtype is not dtype or t.device != device or (shape is not None and t.shape != shape):
-        want = "" if shape is None else f" {list(shape)}"
-        raise W4A8Error(f"{name} must be {str(dtype).replace('torch.', '')}{want} on {device}, got "
-                        f"{str(t.dtype).replace('torch.', '')} {list(t.shape)} on {t.device}")
+    want = "" if shape is None else f" {list(shape)}"
+    raise W4A8Error(f"{name} must be {str(dtype).replace('torch.', '')}{want} on cuda:{index}, got "
+                    f"{str(t.dtype).replace('torch.', '')} {list(t.shape)} on {t.device}")
 
 
-def _launch(device, what, fn, *args):
+def _device_index(t) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise W4A8Error("tensors must live on a CUDA device (no CPU path exists)")
+    return index
+
+
+def _launch(index, what, fn, *args):
     """Calls fn(*args, stream) on the device's current stream, with that device current."""
     torch = _torch()
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
         code = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             code = fn(*args, stream)
     if code != 0:
         raise W4A8Error(f"{what}: {status_string(code)}")
@@ -695,7 +705,7 @@ def rmsnorm_quantize_act(X, weight, eps, residual=None, out=None):
     [M], rowsum int32 [M]); the last three feed gemm. out: the four outputs
     (the first may be X or residual, and is not looked at without a residual)."""
     torch = _torch()
-    dev = X.device
+    dev = _device_index(X)
     if X.dim() != 2:
         raise W4A8Error("X must be a 2-D fp16 tensor")
     M, K = X.shape
@@ -704,9 +714,9 @@ def rmsnorm_quantize_act(X, weight, eps, residual=None, out=None):
     _check_tensor(weight, "weight", f16, dev, (K,))
     if out is None:
         H = None if residual is None else torch.empty_like(X)
-        A8 = torch.empty((M, K), dtype=torch.int8, device=dev)
-        sA = torch.empty((M,), dtype=f16, device=dev)
-        rowsum = torch.empty((M,), dtype=torch.int32, device=dev)
+        A8 = torch.empty((M, K), dtype=torch.int8, device=X.device)
+        sA = torch.empty((M,), dtype=f16, device=X.device)
+        rowsum = torch.empty((M,), dtype=torch.int32, device=X.device)
     else:
         H, A8, sA, rowsum = out
         _check_tensor(A8, "A8", torch.int8, dev, (M, K))
@@ -782,20 +792,18 @@ def kv8_cache(num_pages: int, Hkv: int, page: int = 64, device=None):
             torch.zeros((num_pages, 2, Hkv), dtype=torch.float32, device=device))
 
 
-def _kv8_desc(codes, scales, block_table, seq_lens, device):
+def _kv8_desc(codes, scales, block_table, seq_lens, index):
     """The cache descriptor of a call, its tensors checked."""
     torch = _torch()
-    if codes.dim() != 5 or block_table.dim() != 2:
+    if codes.dim() != 5 or block_table.dim() != 2 or codes.shape[1] != 2:
         raise W4A8Error("kv_codes must be int8 [num_pages, 2, Hkv, page, 128] and block_table int32 [B, max_blocks]")
-    pages, two, Hkv, page, D = codes.shape
-    if two != 2:
-        raise W4A8Error("kv_codes must be int8 [num_pages, 2, Hkv, page, 128]")
-    i32 = torch.int32
-    _check_tensor(codes, "kv_codes", torch.int8, device)
-    _check_tensor(scales, "kv_scales", torch.float32, device, (pages, 2, Hkv))
-    _check_tensor(block_table, "block_table", i32, device)
+    pages, _, Hkv, page, D = codes.shape
     B, blocks = block_table.shape
-    _check_tensor(seq_lens, "seq_lens", i32, device, (B,))
+    i32 = torch.int32
+    _check_tensor(codes, "kv_codes", torch.int8, index)
+    _check_tensor(scales, "kv_scales", torch.float32, index, (pages, 2, Hkv))
+    _check_tensor(block_table, "block_table", i32, index)
+    _check_tensor(seq_lens, "seq_lens", i32, index, (B,))
     return Kv8CacheDesc(codes.data_ptr(), scales.data_ptr(), block_table.data_ptr(), pages, blocks, Hkv, page, D,
                         0), B, Hkv
 
@@ -808,7 +816,7 @@ def kv8_rope_append(qkv, Hq: int, kv_codes, kv_scales, block_table, seq_lens, in
     q_start int32 [B + 1]: its first new row (None: one row per sequence).
     inv_freq fp32 [rotary_dim / 2] and rope_scale as from rope_frequencies."""
     torch = _torch()
-    dev = qkv.device
+    dev = _device_index(qkv)
     desc, B, Hkv = _kv8_desc(kv_codes, kv_scales, block_table, seq_lens, dev)
     if qkv.dim() != 2:
         raise W4A8Error("qkv must be fp16 [T, (Hq + 2 Hkv) * 128]")
@@ -822,7 +830,7 @@ def kv8_rope_append(qkv, Hq: int, kv_codes, kv_scales, block_table, seq_lens, in
         _check_tensor(q_start, "q_start", torch.int32, dev, (B + 1,))
         start = q_start.data_ptr()
     if out is None:
-        out = torch.empty((T, Hq, KV_HEAD_DIM), dtype=f16, device=dev)
+        out = torch.empty((T, Hq, KV_HEAD_DIM), dtype=f16, device=qkv.device)
     else:
         _check_tensor(out, "out", f16, dev, (T, Hq, KV_HEAD_DIM))
     _launch(dev, "w4a8_kv8_rope_append", lib().w4a8_kv8_rope_append, qkv.data_ptr(), desc, seq_lens.data_ptr(), start,
@@ -837,38 +845,39 @@ def kv8_workspace_bytes(B: int, T: int, Hq: int, Hkv: int) -> int:
 _kv8_ws = {}
 
 
-def _kv8_workspace_for(device, nbytes: int):
+def _kv8_workspace_for(q, index, B, T, Hq, Hkv):
     """A zero-filled workspace per stream (calls on different streams may
     overlap), grown on demand and reused; a call that is being captured gets
     one of its own, which its graph zero-fills and keeps."""
     torch = _torch()
+    nbytes = max(kv8_workspace_bytes(B, T, Hq, Hkv), 256)
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+        return torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
+    key = (index, torch._C._cuda_getCurrentRawStream(index))
     ws = _kv8_ws.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = _kv8_ws[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        ws = _kv8_ws[key] = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
     return ws
 
 
 def _kv8_attention(what, q, kv_codes, kv_scales, block_table, seq_lens, scale, q_start, out, workspace):
     torch = _torch()
-    dev = q.device
+    dev = _device_index(q)
     desc, B, Hkv = _kv8_desc(kv_codes, kv_scales, block_table, seq_lens, dev)
     if q.dim() != 3 or q.shape[2] != KV_HEAD_DIM or (q_start is None and q.shape[0] != B):
         raise W4A8Error("q must be fp16 [T, Hq, 128], with one row per sequence for decode")
-    T, Hq, _ = q.shape
+    T, Hq, _ = shape = q.shape
     f16 = torch.float16
     _check_tensor(q, "q", f16, dev)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check_tensor(out, "out", f16, dev, q.shape)
-    L = lib()
+        _check_tensor(out, "out", f16, dev, shape)
     if workspace is None:
-        workspace = _kv8_workspace_for(dev, max(L.w4a8_kv8_attention_workspace_bytes(B, T, Hq, Hkv), 256))
+        workspace = _kv8_workspace_for(q, dev, B, T, Hq, Hkv)
     else:
         _check_tensor(workspace, "workspace", torch.uint8, dev)
+    L = lib()
     if q_start is None:
         _launch(dev, what, L.w4a8_kv8_attention_decode, q.data_ptr(), desc, seq_lens.data_ptr(), B, Hq, scale,
                 out.data_ptr(), workspace.data_ptr(), workspace.numel())
