@@ -540,15 +540,15 @@ typedef struct {
  * head are rotated by the token's position p = seq_lens[b] - n_b + i: pairs (2
  * j, 2 j + 1) if interleaved, else (j, j + rotary_dim / 2),
  *   (a, b) -> rope_scale * (a cos t - b sin t, a sin t + b cos t),  t = p * inv_freq[j],
- * the angle exact to 2^-24 radians at every position (no fp32 product of a
- * large position). inv_freq: fp32 [rotary_dim / 2] in device memory, as scaled
+ * the angle exact to 2^-22 radians at every position (no fp32 product of a
+ * large position), its sine and cosine to 2^-20. inv_freq: fp32 [rotary_dim / 2] in device memory, as scaled
  * for long contexts by the caller; rope_scale: a factor on the rotated values
  * (1 for none).
  * q goes to q_out, fp16 [T, Hq, 128] (16-byte aligned); k and v (as fp32, not
  * rounded in between) into the cache. In every page that gets new tokens
  *   s' = max(s, fp32(max |new values| / 127)),  s = 0 if the page's first place is one of them
  *   codes that were there: rint(code * (s / s')) if s' > s
- *   new codes: clamp(rint(x / s'), -127, 127)   (IEEE divides, ties to even; s' == 0 gives zeros)
+ *   new codes: clamp(rint(x * (1 / s')), -127, 127)   (ties to even; s' == 0 gives zeros)
  * and s' becomes its scale. Places behind the new tokens are left as they are.
  * A page that gets new tokens must not be shared with another sequence of the
  * batch. Non-finite inputs are a precondition violation (that page's contents

@@ -1,9 +1,9 @@
 """The paged 8-bit KV cache: rotation and append, decode and prefill
 attention, against the oracle in 64 bits.
 
-Tolerances, derived. Append: an angle is off by at most 2^-23 turns of pi, the
-sine and cosine by 2^-22, so a rotated value by 2^-20 of its pair's larger
-half (ROT), scale factor included; a page's scale is within 2 ROT of the
+Tolerances, derived. Append: the sine and cosine are within 2^-20.5 (their
+angle within 2^-22), so a rotated value is within 2^-19.5 of its pair's larger
+half, under 2 ROT, scale factor included; a page's scale is within 2 ROT of the
 exact one relatively; with the scale taken as given a new code is within 1/2
 + 127 * 4 ROT of x / s', a carried code within 1/2 + 127 * 2^-22. Attention:
 the oracle's bound plus half an fp16 ulp; the decode kernels keep the

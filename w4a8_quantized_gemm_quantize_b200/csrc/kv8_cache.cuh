@@ -90,31 +90,53 @@ constexpr int kKv8AppendThreads = 256;
 // f_i / (2 pi) is held as a 64-bit fraction of a turn, so that the product
 // with the position wraps at whole turns by itself and is exact to 2^-29 of a
 // turn at position 2^24 (an fp32 product is off by 2^-24 * pos * f radians,
-// 0.008 at position 131072). Its top 32 bits give the angle in half turns.
+// 0.008 at position 131072). Its top 32 bits give the angle in [-pi, pi), where
+// the hardware's sine and cosine are within 2^-20.5: far below a half step of
+// the fp16 (2^-11) or 8-bit (2^-8) values that come of it.
 __device__ __forceinline__ uint64_t kv8_turns(float f) {
   const double t = static_cast<double>(f) * 0.15915494309189533577;  // 1 / (2 pi)
   return static_cast<uint64_t>((t - floor(t)) * 18446744073709551616.0);
 }
 __device__ __forceinline__ float2 kv8_cos_sin(uint64_t turns, int pos, float scale) {
   const int32_t top = static_cast<int32_t>((turns * static_cast<uint64_t>(pos)) >> 32);
-  float s, c;
-  sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-  return make_float2(c * scale, s * scale);
+  const float angle = static_cast<float>(top) * 1.4629180792671596e-9f;  // pi / 2^31
+  return make_float2(__cosf(angle) * scale, __sinf(angle) * scale);
 }
 
-// Elements 8 i .. 8 i + 7 of one head's vector (`vec` points at its 128
-// values), rotated: (a, b) -> (a cos - b sin, a sin + b cos) for the pairs (2
-// j, 2 j + 1) (interleaved) or (j, j + rotary / 2). cs: this token's (cos, sin).
-__device__ __forceinline__ void kv8_rotated(const __half* vec, int i, const float2* cs, int rotary, int interleaved,
-                                            float (&o)[8]) {
-  const uint4 raw = *reinterpret_cast<const uint4*>(vec + 8 * i);
-  const __half2* h = reinterpret_cast<const __half2*>(&raw);
+// Eight values of one head's vector and, in the half layout with whole vectors
+// of partners, the eight that they are rotated with.
+struct Kv8Vec {
+  uint4 v, p;
+};
+__device__ __forceinline__ bool kv8_whole_partners(int rotary, int interleaved) {
+  return !interleaved && ((rotary >> 1) & 7) == 0;
+}
+__device__ __forceinline__ Kv8Vec kv8_load(const __half* vec, int i, int rotary, int interleaved) {
+  Kv8Vec r;
+  r.v = __ldcs(reinterpret_cast<const uint4*>(vec + 8 * i));
+  r.p = r.v;
+  if (8 * i < rotary && kv8_whole_partners(rotary, interleaved)) {
+    const int half = rotary >> 1;
+    r.p = *reinterpret_cast<const uint4*>(vec + 8 * i + (8 * i < half ? half : -half));
+  }
+  return r;
+}
+__device__ __forceinline__ void kv8_to_float(const uint4& v, float (&o)[8]) {
+  const __half2* h = reinterpret_cast<const __half2*>(&v);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 f = __half22float2(h[j]);
     o[2 * j] = f.x;
     o[2 * j + 1] = f.y;
   }
+}
+// Elements 8 i .. 8 i + 7 of a vector, rotated: (a, b) -> (a cos - b sin, a sin
+// + b cos) for the pairs (2 j, 2 j + 1) (interleaved) or (j, j + rotary / 2).
+// cs: this token's (cos, sin) of each pair; vec: the vector (read only where
+// the partners are not whole vectors).
+__device__ __forceinline__ void kv8_rotate(const Kv8Vec& r, const __half* vec, int i, const float2* cs, int rotary,
+                                           int interleaved, float (&o)[8]) {
+  kv8_to_float(r.v, o);
   if (8 * i >= rotary) return;
   const int half = rotary >> 1;
   if (interleaved) {
@@ -130,75 +152,101 @@ __device__ __forceinline__ void kv8_rotated(const __half* vec, int i, const floa
     return;
   }
   float p[8];
-  if ((half & 7) == 0) {  // the partners are another whole vector
+  if ((half & 7) == 0) {
+    kv8_to_float(r.p, p);
     const bool low = 8 * i < half;
-    const uint4 raw2 = *reinterpret_cast<const uint4*>(vec + 8 * i + (low ? half : -half));
-    const __half2* h2 = reinterpret_cast<const __half2*>(&raw2);
+    const float4* c = reinterpret_cast<const float4*>(cs + 8 * i - (low ? 0 : half));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(h2[j]);
-      p[2 * j] = f.x;
-      p[2 * j + 1] = f.y;
+      const float4 t = c[j];  // (cos, sin) of two pairs
+      o[2 * j] = low ? o[2 * j] * t.x - p[2 * j] * t.y : p[2 * j] * t.y + o[2 * j] * t.x;
+      o[2 * j + 1] = low ? o[2 * j + 1] * t.z - p[2 * j + 1] * t.w : p[2 * j + 1] * t.w + o[2 * j + 1] * t.z;
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int d = 8 * i + e;
-      p[e] = d < half ? __half2float(vec[d + half]) : d < rotary ? __half2float(vec[d - half]) : 0.0f;
-    }
+    return;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int d = 8 * i + e;
     if (d < half) {
       const float2 t = cs[d];
-      o[e] = o[e] * t.x - p[e] * t.y;
+      o[e] = o[e] * t.x - __half2float(vec[d + half]) * t.y;
     } else if (d < rotary) {
       const float2 t = cs[d - half];
-      o[e] = p[e] * t.y + o[e] * t.x;
+      o[e] = __half2float(vec[d - half]) * t.y + o[e] * t.x;
     }
   }
 }
 
-// Blocks [0, q_blocks): q_rows rows of q each, every head of them (the angles
-// are worked out once a row). The others: one (page of a sequence, K | V,
-// head) each; P * 16 vectors of 8 values, in registers from the read to the
-// codes, so that the maximum over the page comes before the first code.
+// Blocks [0, q_blocks): q_rows (at most 4) rows of q each, every head of them,
+// so that the angles are worked out once a row. The others: one (page of a
+// sequence, K | V, head) each; P * 16 vectors of 8 values, in registers from
+// the read to the codes, so that the maximum over the page comes before the
+// first code.
+//
+// HBM-bound (2 bytes read per value, 2 or 1 written) for many rows; a decode
+// step is a chain of dependent reads (length, table, page scale). All of a
+// thread's reads are under way before the angles are worked out.
 template <int P>
 __global__ void __launch_bounds__(kKv8AppendThreads) kv8_append_kernel(Kv8AppendArgs a) {
   constexpr int kSlab = kKv8AppendThreads / 16;  // tokens of the page a pass covers
   constexpr int kPasses = P / kSlab;
-  __shared__ float2 s_cs[kSlab][kKv8D / 2];  // (cos, sin) of a slab's tokens
+  __shared__ uint64_t s_turns[kKv8D / 2];
+  __shared__ __align__(16) float2 s_cs[2][kSlab][kKv8D / 2];  // (cos, sin) of a slab's tokens, two turns
   __shared__ float s_red[kKv8AppendThreads / 32];
-  grid_dependency_wait();
-  grid_launch_dependents();
   const int t = threadIdx.x;
   const int half = a.rotary >> 1;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (t < half) s_turns[t] = kv8_turns(__ldg(a.inv_freq + t));
   const int64_t capacity = static_cast<int64_t>(a.c.max_blocks) * P;
   const int64_t row_elems = static_cast<int64_t>(a.Hq + 2 * a.c.Hkv) * kKv8D;
   if (static_cast<int>(blockIdx.x) < a.q_blocks) {
-    for (int k = 0; k < a.q_rows; ++k) {
-      const int row = static_cast<int>(blockIdx.x) * a.q_rows + k;
-      if (row >= a.s.T) break;
-      const int b = a.s.q_start == nullptr ? row : kv8_find(a.s, row, 1, 1, 0);
-      if (b < 0) continue;
-      const Kv8Seq q = kv8_sequence(a.s, b, capacity, t == 0 ? a.err : nullptr);
-      if (row - q.first >= q.n) continue;  // behind the last sequence, or not a valid one: left as it is
-      const int pos = q.pos0 + row - q.first;
-      __syncthreads();
-      for (int i = t; i < half; i += kKv8AppendThreads)
-        s_cs[0][i] = kv8_cos_sin(kv8_turns(__ldg(a.inv_freq + i)), pos, a.rope_scale);
-      __syncthreads();
-      const __half* src = a.qkv + row * row_elems;
-      __half* dst = a.q_out + static_cast<int64_t>(row) * a.Hq * kKv8D;
-      for (int v = t; v < a.Hq * 16; v += kKv8AppendThreads) {
-        float o[8];
-        kv8_rotated(src + (v >> 4) * kKv8D, v & 15, s_cs[0], a.rotary, a.interleaved, o);
-        uint4 pack;
-        __half2* h = reinterpret_cast<__half2*>(&pack);
+    const int row0 = static_cast<int>(blockIdx.x) * a.q_rows;
+    // every row's position, -1 for one that is left as it is
+    int pos[4] = {-1, -1, -1, -1};
+    Kv8Seq q = {0, -1, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(o[2 * j], o[2 * j + 1]);
-        reinterpret_cast<uint4*>(dst)[v] = pack;
+    for (int k = 0; k < 4; ++k) {
+      const int row = row0 + k;
+      if (k >= a.q_rows || row >= a.s.T) break;
+      if (k == 0 || row - q.first >= q.n) {
+        const int b = a.s.q_start == nullptr ? row : kv8_find(a.s, row, 1, 1, 0);
+        if (b < 0) continue;
+        q = kv8_sequence(a.s, b, capacity, t == 0 ? a.err : nullptr);
+      }
+      if (row - q.first < q.n) pos[k] = q.pos0 + row - q.first;
+    }
+    __syncthreads();
+    {
+      const int k = t >> 6, f = t & 63;
+      const int p = k == 0 ? pos[0] : k == 1 ? pos[1] : k == 2 ? pos[2] : pos[3];
+      if (f < half && p >= 0) s_cs[0][k][f] = kv8_cos_sin(s_turns[f], p, a.rope_scale);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (pos[k] < 0) continue;
+      const __half* src = a.qkv + (row0 + k) * row_elems;
+      uint4* dst = reinterpret_cast<uint4*>(a.q_out + static_cast<int64_t>(row0 + k) * a.Hq * kKv8D);
+      for (int v0 = t; v0 < a.Hq * 16; v0 += 2 * kKv8AppendThreads) {
+        Kv8Vec r[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int v = v0 + u * kKv8AppendThreads;
+          if (v < a.Hq * 16) r[u] = kv8_load(src + (v >> 4) * kKv8D, v & 15, a.rotary, a.interleaved);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int v = v0 + u * kKv8AppendThreads;
+          if (v >= a.Hq * 16) break;
+          float o[8];
+          kv8_rotate(r[u], src + (v >> 4) * kKv8D, v & 15, s_cs[0][k], a.rotary, a.interleaved, o);
+          uint4 pack;
+          __half2* h = reinterpret_cast<__half2*>(&pack);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(o[2 * j], o[2 * j + 1]);
+          dst[v] = pack;
+        }
       }
     }
     return;
@@ -222,8 +270,19 @@ __global__ void __launch_bounds__(kKv8AppendThreads) kv8_append_kernel(Kv8Append
   if (q.n <= 0) return;
   const int page_no = q.pos0 / P + k;
   if (page_no > (q.len - 1) / P) return;
-  const int base = page_no * P;                           // position of the page's first place
+  const int base = page_no * P;                                     // position of the page's first place
   const int lo = max(q.pos0 - base, 0), hi = min(q.len - base, P);  // places [lo, hi) are new
+  const bool is_k = kh < a.c.Hkv;
+  const int rotary = is_k ? a.rotary : 0;
+  const __half* src = a.qkv + (static_cast<int64_t>(q.first) + base - q.pos0) * row_elems +
+                      static_cast<int64_t>(a.Hq + kh) * kKv8D;  // place 0 of the page (read from place lo on)
+  const int i = t & 15;
+  Kv8Vec raw[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int j = p * kSlab + (t >> 4);
+    if (j >= lo && j < hi) raw[p] = kv8_load(src + j * row_elems, i, rotary, a.interleaved);
+  }
   const int page = __ldg(a.c.table + static_cast<int64_t>(b) * a.c.max_blocks + page_no);
   if (page < 0 || page >= a.c.num_pages) {
     if (t == 0) atomicCAS(a.err, 0, kErrKv8Range);
@@ -231,46 +290,42 @@ __global__ void __launch_bounds__(kKv8AppendThreads) kv8_append_kernel(Kv8Append
   }
   const int64_t block = static_cast<int64_t>(page) * heads2 + kh;
   int8_t* codes = a.c.codes + block * P * kKv8D;
-  const bool is_k = kh < a.c.Hkv;
-  const __half* src = a.qkv + (static_cast<int64_t>(q.first) + base - q.pos0) * row_elems +
-                      static_cast<int64_t>(a.Hq + kh) * kKv8D;  // place 0 of the page (read from place lo on)
-  const int i = t & 15;
+  const float s_old = lo > 0 ? a.c.scales[block] : 0.0f;
   float x[kPasses][8];
   float amax = 0.0f;
+  if (is_k) __syncthreads();  // s_turns
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int j = p * kSlab + (t >> 4);
-    if (is_k && (p + 1) * kSlab > lo && p * kSlab < hi) {  // the slab holds new tokens
-      __syncthreads();
-      for (int f = t & 15; f < half; f += 16)
-        s_cs[t >> 4][f] = kv8_cos_sin(kv8_turns(__ldg(a.inv_freq + f)), base + j, a.rope_scale);
-      __syncthreads();
+    const bool some = (p + 1) * kSlab > lo && p * kSlab < hi;  // the slab holds new tokens
+    if (is_k && some) {
+      for (int f = i; f < half; f += 16)
+        s_cs[p & 1][t >> 4][f] = kv8_cos_sin(s_turns[f], base + j, a.rope_scale);
+      __syncthreads();  // (a slab's angles are overwritten two slabs, one barrier, later)
     }
     if (j >= lo && j < hi) {
-      kv8_rotated(src + j * row_elems, i, s_cs[t >> 4], is_k ? a.rotary : 0, a.interleaved, x[p]);
+      kv8_rotate(raw[p], src + j * row_elems, i, s_cs[p & 1][t >> 4], rotary, a.interleaved, x[p]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[p][e]));
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float s_old = lo > 0 ? a.c.scales[block] : 0.0f;
   if ((t & 31) == 0) s_red[t >> 5] = amax;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kKv8AppendThreads / 32; ++w) amax = fmaxf(amax, s_red[w]);
   const float s_new = fmaxf(s_old, __fdiv_rn(amax, 127.0f));
+  const float r = s_new > 0.0f ? __fdiv_rn(1.0f, s_new) : 0.0f;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int j = p * kSlab + (t >> 4);
     if (j >= lo && j < hi) {
       uint32_t w[2] = {0u, 0u};
-      if (s_new > 0.0f) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = max(-127, min(127, __float2int_rn(__fdiv_rn(x[p][e], s_new))));
-          w[e >> 2] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (e & 3));
-        }
+      for (int e = 0; e < 8; ++e) {
+        const int c = max(-127, min(127, __float2int_rn(x[p][e] * r)));
+        w[e >> 2] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (e & 3));
       }
       *reinterpret_cast<uint2*>(codes + j * kKv8D + 8 * i) = make_uint2(w[0], w[1]);
     }
