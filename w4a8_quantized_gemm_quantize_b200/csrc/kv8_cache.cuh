@@ -79,7 +79,7 @@ struct Kv8AppendArgs {
   Kv8Batch s;
   const float* inv_freq;  // [rotary / 2]
   __half* q_out;          // [T, Hq, 128]
-  int Hq, rotary, interleaved, q_rows, q_blocks;
+  int Hq, rotary, q_rows, q_blocks;
   float rope_scale;
   int* err;
 };
@@ -97,82 +97,79 @@ __device__ __forceinline__ uint64_t kv8_turns(float f) {
   const double t = static_cast<double>(f) * 0.15915494309189533577;  // 1 / (2 pi)
   return static_cast<uint64_t>((t - floor(t)) * 18446744073709551616.0);
 }
-__device__ __forceinline__ float2 kv8_cos_sin(uint64_t turns, int pos, float scale) {
+__device__ __forceinline__ void kv8_cos_sin(uint64_t turns, int pos, float scale, float* c, float* s) {
   const int32_t top = static_cast<int32_t>((turns * static_cast<uint64_t>(pos)) >> 32);
   const float angle = static_cast<float>(top) * 1.4629180792671596e-9f;  // pi / 2^31
-  return make_float2(__cosf(angle) * scale, __sinf(angle) * scale);
+  *c = __cosf(angle) * scale;
+  *s = __sinf(angle) * scale;
 }
 
-// Eight values of one head's vector and, in the half layout with whole vectors
-// of partners, the eight that they are rotated with.
-struct Kv8Vec {
-  uint4 v, p;
+// Which eight of a head's 128 values lane i of 16 takes: [lo, lo + 4) and [hi,
+// hi + 4), whole pairs where that can be, so that each is rotated once.
+//  kSplit: half layout, pairs (j, j + rotary / 2): j = 4 i .. in the first rotary
+//    / 8 lanes, the values behind the rotated ones in the others;
+//  kPairs: interleaved pairs, the eight in a row from 8 i;
+//  kSingle: what fours do not divide (half layout with rotary % 8 != 0): the
+//    eight in a row, each pair's other value read by itself.
+enum Kv8Layout { kSplit, kPairs, kSingle };
+struct Kv8Lane {
+  int lo, hi;
 };
-__device__ __forceinline__ bool kv8_whole_partners(int rotary, int interleaved) {
-  return !interleaved && ((rotary >> 1) & 7) == 0;
-}
-__device__ __forceinline__ Kv8Vec kv8_load(const __half* vec, int i, int rotary, int interleaved) {
-  Kv8Vec r;
-  r.v = __ldcs(reinterpret_cast<const uint4*>(vec + 8 * i));
-  r.p = r.v;
-  if (8 * i < rotary && kv8_whole_partners(rotary, interleaved)) {
+template <Kv8Layout L>
+__device__ __forceinline__ Kv8Lane kv8_lane(int i, int rotary) {
+  if constexpr (L == kSplit) {
     const int half = rotary >> 1;
-    r.p = *reinterpret_cast<const uint4*>(vec + 8 * i + (8 * i < half ? half : -half));
+    if (4 * i < half) return {4 * i, half + 4 * i};
+    return {rotary + 8 * (i - half / 4), rotary + 8 * (i - half / 4) + 4};
   }
-  return r;
+  return {8 * i, 8 * i + 4};
 }
-__device__ __forceinline__ void kv8_to_float(const uint4& v, float (&o)[8]) {
-  const __half2* h = reinterpret_cast<const __half2*>(&v);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = __half22float2(h[j]);
-    o[2 * j] = f.x;
-    o[2 * j + 1] = f.y;
-  }
+struct Kv8Vec {
+  uint2 lo, hi;
+};
+__device__ __forceinline__ Kv8Vec kv8_load(const __half* vec, const Kv8Lane& n) {
+  return {__ldcs(reinterpret_cast<const uint2*>(vec + n.lo)), __ldcs(reinterpret_cast<const uint2*>(vec + n.hi))};
 }
-// Elements 8 i .. 8 i + 7 of a vector, rotated: (a, b) -> (a cos - b sin, a sin
-// + b cos) for the pairs (2 j, 2 j + 1) (interleaved) or (j, j + rotary / 2).
-// cs: this token's (cos, sin) of each pair; vec: the vector (read only where
-// the partners are not whole vectors).
-__device__ __forceinline__ void kv8_rotate(const Kv8Vec& r, const __half* vec, int i, const float2* cs, int rotary,
-                                           int interleaved, float (&o)[8]) {
-  kv8_to_float(r.v, o);
-  if (8 * i >= rotary) return;
+__device__ __forceinline__ void kv8_to_float(const uint2& v, float* o) {
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+  o[0] = a.x;
+  o[1] = a.y;
+  o[2] = b.x;
+  o[3] = b.y;
+}
+// The lane's values (o[0..3] from lo, o[4..7] from hi), rotated: (a, b) -> (a
+// cos - b sin, a sin + b cos). c, s: this token's cosine and sine of each pair;
+// vec: the vector (kSingle).
+template <Kv8Layout L>
+__device__ __forceinline__ void kv8_rotate(const Kv8Vec& r, const __half* vec, int i, const float* c, const float* s,
+                                           int rotary, float (&o)[8]) {
+  kv8_to_float(r.lo, o);
+  kv8_to_float(r.hi, o + 4);
   const int half = rotary >> 1;
-  if (interleaved) {
+  if constexpr (L == kSingle) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (8 * i + 2 * j < rotary) {
-        const float2 t = cs[4 * i + j];
-        const float a = o[2 * j], b = o[2 * j + 1];
-        o[2 * j] = a * t.x - b * t.y;
-        o[2 * j + 1] = a * t.y + b * t.x;
+    for (int e = 0; e < 8; ++e) {
+      const int d = 8 * i + e;
+      if (d < rotary) {
+        const int j = d < half ? d : d - half;
+        const float y = __half2float(vec[d < half ? d + half : j]);
+        o[e] = d < half ? o[e] * c[j] - y * s[j] : y * s[j] + o[e] * c[j];
       }
     }
-    return;
-  }
-  float p[8];
-  if ((half & 7) == 0) {
-    kv8_to_float(r.p, p);
-    const bool low = 8 * i < half;
-    const float4* c = reinterpret_cast<const float4*>(cs + 8 * i - (low ? 0 : half));
+  } else if (4 * i < half) {
+    // (kPairs: a rotary that 8 does not divide ends inside a lane's pairs)
+    const float4 cv = *reinterpret_cast<const float4*>(c + 4 * i), sv = *reinterpret_cast<const float4*>(s + 4 * i);
+    const float ca[4] = {cv.x, cv.y, cv.z, cv.w}, sa[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 t = c[j];  // (cos, sin) of two pairs
-      o[2 * j] = low ? o[2 * j] * t.x - p[2 * j] * t.y : p[2 * j] * t.y + o[2 * j] * t.x;
-      o[2 * j + 1] = low ? o[2 * j + 1] * t.z - p[2 * j + 1] * t.w : p[2 * j + 1] * t.w + o[2 * j + 1] * t.z;
-    }
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int d = 8 * i + e;
-    if (d < half) {
-      const float2 t = cs[d];
-      o[e] = o[e] * t.x - __half2float(vec[d + half]) * t.y;
-    } else if (d < rotary) {
-      const float2 t = cs[d - half];
-      o[e] = __half2float(vec[d - half]) * t.y + o[e] * t.x;
+    for (int e = 0; e < 4; ++e) {
+      float& x = o[L == kSplit ? e : 2 * e];
+      float& y = o[L == kSplit ? e + 4 : 2 * e + 1];
+      const float u = x * ca[e] - y * sa[e], v = x * sa[e] + y * ca[e];
+      if (L == kSplit || 4 * i + e < half) {
+        x = u;
+        y = v;
+      }
     }
   }
 }
@@ -186,14 +183,15 @@ __device__ __forceinline__ void kv8_rotate(const Kv8Vec& r, const __half* vec, i
 // HBM-bound (2 bytes read per value, 2 or 1 written) for many rows; a decode
 // step is a chain of dependent reads (length, table, page scale). All of a
 // thread's reads are under way before the angles are worked out.
-template <int P>
-__global__ void __launch_bounds__(kKv8AppendThreads) kv8_append_kernel(Kv8AppendArgs a) {
+template <int P, Kv8Layout L>
+__global__ void __launch_bounds__(kKv8AppendThreads, P <= 64 ? 4 : 2) kv8_append_kernel(Kv8AppendArgs a) {
   constexpr int kSlab = kKv8AppendThreads / 16;  // tokens of the page a pass covers
   constexpr int kPasses = P / kSlab;
   __shared__ uint64_t s_turns[kKv8D / 2];
-  __shared__ __align__(16) float2 s_cs[2][kSlab][kKv8D / 2];  // (cos, sin) of a slab's tokens, two turns
+  __shared__ __align__(16) float s_cos[2][kSlab][kKv8D / 2], s_sin[2][kSlab][kKv8D / 2];  // of a slab's tokens, two turns
   __shared__ float s_red[kKv8AppendThreads / 32];
   const int t = threadIdx.x;
+  const int i = t & 15;  // lane of a vector
   const int half = a.rotary >> 1;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -202,6 +200,7 @@ __global__ void __launch_bounds__(kKv8AppendThreads) kv8_append_kernel(Kv8Append
   const int64_t row_elems = static_cast<int64_t>(a.Hq + 2 * a.c.Hkv) * kKv8D;
   if (static_cast<int>(blockIdx.x) < a.q_blocks) {
     const int row0 = static_cast<int>(blockIdx.x) * a.q_rows;
+    const Kv8Lane lane = kv8_lane<L>(i, a.rotary);
     // every row's position, -1 for one that is left as it is
     int pos[4] = {-1, -1, -1, -1};
     Kv8Seq q = {0, -1, 0, 0};
@@ -220,32 +219,33 @@ __global__ void __launch_bounds__(kKv8AppendThreads) kv8_append_kernel(Kv8Append
     {
       const int k = t >> 6, f = t & 63;
       const int p = k == 0 ? pos[0] : k == 1 ? pos[1] : k == 2 ? pos[2] : pos[3];
-      if (f < half && p >= 0) s_cs[0][k][f] = kv8_cos_sin(s_turns[f], p, a.rope_scale);
+      if (f < half && p >= 0) kv8_cos_sin(s_turns[f], p, a.rope_scale, &s_cos[0][k][f], &s_sin[0][k][f]);
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (pos[k] < 0) continue;
       const __half* src = a.qkv + (row0 + k) * row_elems;
-      uint4* dst = reinterpret_cast<uint4*>(a.q_out + static_cast<int64_t>(row0 + k) * a.Hq * kKv8D);
+      __half* dst = a.q_out + static_cast<int64_t>(row0 + k) * a.Hq * kKv8D;
       for (int v0 = t; v0 < a.Hq * 16; v0 += 2 * kKv8AppendThreads) {
         Kv8Vec r[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int v = v0 + u * kKv8AppendThreads;
-          if (v < a.Hq * 16) r[u] = kv8_load(src + (v >> 4) * kKv8D, v & 15, a.rotary, a.interleaved);
+          if (v < a.Hq * 16) r[u] = kv8_load(src + (v >> 4) * kKv8D, lane);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int v = v0 + u * kKv8AppendThreads;
           if (v >= a.Hq * 16) break;
           float o[8];
-          kv8_rotate(r[u], src + (v >> 4) * kKv8D, v & 15, s_cs[0][k], a.rotary, a.interleaved, o);
-          uint4 pack;
-          __half2* h = reinterpret_cast<__half2*>(&pack);
+          kv8_rotate<L>(r[u], src + (v >> 4) * kKv8D, i, s_cos[0][k], s_sin[0][k], a.rotary, o);
+          uint2 w[2];
+          __half2* h = reinterpret_cast<__half2*>(w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(o[2 * j], o[2 * j + 1]);
-          dst[v] = pack;
+          *reinterpret_cast<uint2*>(dst + (v >> 4) * kKv8D + lane.lo) = w[0];
+          *reinterpret_cast<uint2*>(dst + (v >> 4) * kKv8D + lane.hi) = w[1];
         }
       }
     }
@@ -276,12 +276,12 @@ __global__ void __launch_bounds__(kKv8AppendThreads) kv8_append_kernel(Kv8Append
   const int rotary = is_k ? a.rotary : 0;
   const __half* src = a.qkv + (static_cast<int64_t>(q.first) + base - q.pos0) * row_elems +
                       static_cast<int64_t>(a.Hq + kh) * kKv8D;  // place 0 of the page (read from place lo on)
-  const int i = t & 15;
+  const Kv8Lane lane = kv8_lane<L>(i, rotary);
   Kv8Vec raw[kPasses];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int j = p * kSlab + (t >> 4);
-    if (j >= lo && j < hi) raw[p] = kv8_load(src + j * row_elems, i, rotary, a.interleaved);
+    if (j >= lo && j < hi) raw[p] = kv8_load(src + j * row_elems, lane);
   }
   const int page = __ldg(a.c.table + static_cast<int64_t>(b) * a.c.max_blocks + page_no);
   if (page < 0 || page >= a.c.num_pages) {
@@ -300,11 +300,11 @@ __global__ void __launch_bounds__(kKv8AppendThreads) kv8_append_kernel(Kv8Append
     const bool some = (p + 1) * kSlab > lo && p * kSlab < hi;  // the slab holds new tokens
     if (is_k && some) {
       for (int f = i; f < half; f += 16)
-        s_cs[p & 1][t >> 4][f] = kv8_cos_sin(s_turns[f], base + j, a.rope_scale);
+        kv8_cos_sin(s_turns[f], base + j, a.rope_scale, &s_cos[p & 1][t >> 4][f], &s_sin[p & 1][t >> 4][f]);
       __syncthreads();  // (a slab's angles are overwritten two slabs, one barrier, later)
     }
     if (j >= lo && j < hi) {
-      kv8_rotate(raw[p], src + j * row_elems, i, s_cs[p & 1][t >> 4], rotary, a.interleaved, x[p]);
+      kv8_rotate<L>(raw[p], src + j * row_elems, i, s_cos[p & 1][t >> 4], s_sin[p & 1][t >> 4], rotary, x[p]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[p][e]));
     }
@@ -327,7 +327,8 @@ __global__ void __launch_bounds__(kKv8AppendThreads) kv8_append_kernel(Kv8Append
         const int c = max(-127, min(127, __float2int_rn(x[p][e] * r)));
         w[e >> 2] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (e & 3));
       }
-      *reinterpret_cast<uint2*>(codes + j * kKv8D + 8 * i) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.lo) = w[0];
+      *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.hi) = w[1];
     }
   }
   if (lo > 0 && s_new > s_old) {  // the codes that were there, carried over to the larger scale

@@ -51,6 +51,17 @@ Kv8Cache kv8_cache_args(const w4a8_kv8_cache_t* c) {
           c->Hkv, c->page};
 }
 
+template <Kv8Layout L>
+w4a8_status_t launch_kv8_append(int page, dim3 grid, cudaStream_t st, const Kv8AppendArgs& a) {
+  const dim3 block(kKv8AppendThreads);
+  switch (page) {
+    case 16: return launch_pdl(kv8_append_kernel<16, L>, grid, block, 0, st, 1, a);
+    case 32: return launch_pdl(kv8_append_kernel<32, L>, grid, block, 0, st, 1, a);
+    case 64: return launch_pdl(kv8_append_kernel<64, L>, grid, block, 0, st, 1, a);
+    default: return launch_pdl(kv8_append_kernel<128, L>, grid, block, 0, st, 1, a);
+  }
+}
+
 // The cache's codes as rows of 128 bytes, loaded in boxes of a decode tile's
 // rows (a page's, where that is smaller) with the 128-byte swizzle.
 w4a8_status_t kv8_map(const w4a8_kv8_cache_t* c, int box_rows, CUtensorMap* map) {
@@ -209,7 +220,6 @@ w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cache_t* cach
   a.q_out = static_cast<__half*>(q_out);
   a.Hq = static_cast<int>(Hq);
   a.rotary = rotary_dim;
-  a.interleaved = interleaved;
   a.rope_scale = rope_scale;
   a.err = dev->err;
   a.q_rows = T > 8 * dev->sms ? 4 : 1;
@@ -217,14 +227,11 @@ w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cache_t* cach
   const int64_t items = q_start == nullptr ? B : T / cache->page + 2 * B;
   const int64_t grid = a.q_blocks + items * 2 * cache->Hkv;
   if (grid > INT32_MAX) return W4A8_ERR_UNSUPPORTED_SHAPE;
-  const dim3 g(static_cast<unsigned>(grid)), block(kKv8AppendThreads);
+  const dim3 g(static_cast<unsigned>(grid));
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  switch (cache->page) {
-    case 16: return launch_pdl(kv8_append_kernel<16>, g, block, 0, cs, 1, a);
-    case 32: return launch_pdl(kv8_append_kernel<32>, g, block, 0, cs, 1, a);
-    case 64: return launch_pdl(kv8_append_kernel<64>, g, block, 0, cs, 1, a);
-    default: return launch_pdl(kv8_append_kernel<128>, g, block, 0, cs, 1, a);
-  }
+  if (interleaved) return launch_kv8_append<kPairs>(cache->page, g, cs, a);
+  if (rotary_dim % 8 == 0) return launch_kv8_append<kSplit>(cache->page, g, cs, a);
+  return launch_kv8_append<kSingle>(cache->page, g, cs, a);
 }
 
 size_t w4a8_kv8_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
