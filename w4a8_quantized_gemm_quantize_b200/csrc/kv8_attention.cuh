@@ -100,26 +100,35 @@ __device__ __forceinline__ void kv8_wait(uint64_t* bar, uint32_t parity, DevErr 
 // then, where a pair crosses CTAs, in the workspace, where the last CTA to
 // arrive (a counter, no waiting) adds them up in the order of the line.
 constexpr int kDecTile = 32;
-constexpr int kDecWarps = 8;
-constexpr int kDecStages = 3;
 constexpr int kDecStageBytes = 2 * kDecTile * kKv8D;
-constexpr int kDecRingBytes = kDecStages * kDecStageBytes;
 constexpr int kDecCols = 8;
-constexpr int kDecPart = kDecCols * (2 + kKv8D);  // floats: m[8], l[8], O[8][128]
+constexpr int kDecPart = kDecCols * (2 + kKv8D);  // floats of a partial result in the workspace: m[8], l[8], O[8][128]
 constexpr int kDecMaxCtas = 256;
 
-// Shared memory of one CTA (offsets from a 1024-byte aligned base): the rings,
-// each warp's first partial result (its last one goes into its spent ring),
-// barriers, the tiles' scales, and what the partial results are of.
-struct DecSmem {
-  static constexpr int kOffPart = kDecWarps * kDecRingBytes;
-  static constexpr int kOffPairs = kOffPart + kDecWarps * kDecPart * 4;
-  static constexpr int kOffBars = kOffPairs + kDecWarps * 2 * 32;
-  static constexpr int kOffMeta = kOffBars + kDecWarps * kDecStages * 8;
-  static constexpr int kOffLast = kOffMeta + kDecWarps * kDecStages * 16;
+// One CTA per SM. Up to four columns (DUP): 12 warps with two stages each
+// (measured, 16 sequences of 2048 to 4096 tokens, 8 kv heads: 8 warps with three
+// stages XX us, 12 with two XX us: the warps wait for their own chains of
+// instructions, not for the copies); up to eight: 10 warps, whose partial
+// results take twice the room.
+template <bool DUP>
+struct DecCfg {
+  static constexpr int kWarps = DUP ? 12 : 10;
+  static constexpr int kStages = 2;
+  static constexpr int kCols = DUP ? 4 : kDecCols;
+  static constexpr int kRingBytes = kStages * kDecStageBytes;
+  static constexpr int kPartBytes = kCols * (2 + kKv8D) * 4;  // m[], l[], O[][128]
+  // Shared memory (offsets from a 1024-byte aligned base): the rings, each
+  // warp's first partial result (its last one goes into its spent ring), what
+  // the partial results are of, barriers, the tiles' scales.
+  static constexpr int kOffPart = kWarps * kRingBytes;
+  static constexpr int kOffPairs = kOffPart + kWarps * kPartBytes;
+  static constexpr int kOffBars = kOffPairs + kWarps * 2 * 32;
+  static constexpr int kOffMeta = kOffBars + kWarps * kStages * 8;
+  static constexpr int kOffLast = kOffMeta + kWarps * kStages * 16;
   static constexpr int kBytes = kOffLast + 16 + 1024;  // + alignment slack
   static_assert(kBytes <= 232448, "shared memory of one CTA");
-  static_assert(kDecPart * 4 <= kDecRingBytes && kOffMeta % 16 == 0, "layout");
+  static_assert(kPartBytes <= kRingBytes && kPartBytes % 16 == 0 && kOffMeta % 16 == 0, "layout");
+  static_assert(2 * kWarps <= 32, "a lane for each partial result when they are joined");
 };
 
 struct Kv8DecodeArgs {
@@ -136,7 +145,7 @@ struct DecPair {
   int row0, n;     // its first row of the batch, its new tokens
   int64_t first;   // the pair's first tile in the line
 };
-static_assert(sizeof(DecPair) == 32, "DecSmem");
+static_assert(sizeof(DecPair) == 32, "DecCfg");
 
 // Sequence b's lengths; tiles == 0: it has no part in this kernel's work.
 __device__ __forceinline__ DecPair dec_sequence(const Kv8AttnArgs& a, int b, int G, int max_rows, bool report) {
@@ -157,20 +166,17 @@ __device__ __forceinline__ DecPair dec_sequence(const Kv8AttnArgs& a, int b, int
 }
 
 // Adds partial result (m2, l2, o2) to (m, l, o), m in powers of two.
-__device__ __forceinline__ void dec_join(float& m, float& l, float4& o, float m2, float l2, float4 o2) {
+__device__ __forceinline__ void dec_join(float& m, float& l, float2& o, float m2, float l2, float2 o2) {
   const float mn = fmaxf(m, m2);
   const float f = m == -INFINITY ? 0.0f : ex2(m - mn), f2 = m2 == -INFINITY ? 0.0f : ex2(m2 - mn);
   m = mn;
   l = l * f + l2 * f2;
   o.x = o.x * f + o2.x * f2;
   o.y = o.y * f + o2.y * f2;
-  o.z = o.z * f + o2.z * f2;
-  o.w = o.w * f + o2.w * f2;
 }
-__device__ __forceinline__ uint2 dec_pack(float4 o, float l) {
+__device__ __forceinline__ __half2 dec_pack(float2 o, float l) {
   const float r = l > 0.0f ? 1.0f / l : 0.0f;
-  const __half2 a = __floats2half2_rn(o.x * r, o.y * r), b = __floats2half2_rn(o.z * r, o.w * r);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  return __floats2half2_rn(o.x * r, o.y * r);
 }
 
 // Where row R of a sequence's kv head lies in q and out.
@@ -179,52 +185,60 @@ __device__ __forceinline__ int64_t dec_row(const Kv8AttnArgs& a, const DecPair& 
 }
 
 template <bool DUP>
-__global__ void __launch_bounds__(kDecWarps * 32, 1)
+__global__ void __launch_bounds__(DecCfg<DUP>::kWarps * 32, 1)
     kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8DecodeArgs args) {
+  using C = DecCfg<DUP>;
+  constexpr int kWarps = C::kWarps, kStages = C::kStages, kCols = C::kCols;
   extern __shared__ __align__(1024) uint8_t dec_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dec_smem_raw) + 1023) & ~uintptr_t(1023));
   const Kv8AttnArgs& a = args.a;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, c = lane & 3;
-  uint8_t* ring = sm + warp * kDecRingBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + DecSmem::kOffBars) + warp * kDecStages;
-  float* meta = reinterpret_cast<float*>(sm + DecSmem::kOffMeta) + warp * kDecStages * 4;
-  DecPair* s_pairs = reinterpret_cast<DecPair*>(sm + DecSmem::kOffPairs);  // [warp][2]
-  int* s_last = reinterpret_cast<int*>(sm + DecSmem::kOffLast);
+  uint8_t* ring = sm + warp * C::kRingBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBars) + warp * kStages;
+  float* meta = reinterpret_cast<float*>(sm + C::kOffMeta) + warp * kStages * 4;
+  DecPair* s_pairs = reinterpret_cast<DecPair*>(sm + C::kOffPairs);  // [warp][2]
+  int* s_last = reinterpret_cast<int*>(sm + C::kOffLast);
   const auto part_of = [&](int entry) {  // a warp's first or last partial result
-    return reinterpret_cast<float*>(entry & 1 ? sm + (entry >> 1) * kDecRingBytes
-                                              : sm + DecSmem::kOffPart + (entry >> 1) * kDecPart * 4);
+    return reinterpret_cast<float*>(entry & 1 ? sm + (entry >> 1) * C::kRingBytes
+                                              : sm + C::kOffPart + (entry >> 1) * C::kPartBytes);
   };
   const DevErr err{a.err};
   const int P = a.c.P, G = a.Hq / a.c.Hkv;
-  const auto groups_of = [&](int n) { return (n * G + kDecCols - 1) / kDecCols; };
-  if (lane < kDecStages) mbar_init(bars + lane, 5);  // the bulk copies, and four scales
+  const int shift = __ffs(P) - 1;
+  const auto groups_of = [&](int n) { return DUP ? 1 : (n * G + kDecCols - 1) / kDecCols; };
+  if (t == 0) prefetch_tensormap(&map);
+  if (lane < kStages) mbar_init(bars + lane, 5);  // the bulk copies, and four scales
   fence_barrier_init();
   __syncwarp();
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // the line's length, and this CTA's and this warp's part of it
-  int64_t total = 0;
-  for (int b = lane; b < a.s.B; b += 32) {
-    const DecPair p = dec_sequence(a, b, G, args.max_rows, blockIdx.x == 0 && warp == 0);
-    total += static_cast<int64_t>(p.tiles) * groups_of(p.n) * a.c.Hkv;
-  }
+  // the line's length, and this CTA's and this warp's part of it (mine: of up to
+  // 32 sequences, looked up once)
+  const auto work_of = [&](const DecPair& p) { return static_cast<int64_t>(p.tiles) * (groups_of(p.n) * a.c.Hkv); };
+  DecPair mine = dec_sequence(a, lane, G, args.max_rows, blockIdx.x == 0 && warp == 0);
+  int64_t total = work_of(mine);
+  for (int b = lane + 32; b < a.s.B; b += 32)
+    total += work_of(dec_sequence(a, b, G, args.max_rows, blockIdx.x == 0 && warp == 0));
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (total == 0) return;
-  const int64_t want = (total + kDecWarps - 1) / kDecWarps;
+  const int64_t want = (total + kWarps - 1) / kWarps;
   const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
   if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const auto cta_start = [&](int64_t i) { return i * total / ctas; };
+  // CTA i takes quot tiles, one more if i < rest
+  const int64_t quot = total / ctas;
+  const int rest = static_cast<int>(total - quot * ctas);
+  const auto cta_start = [&](int i) { return i * quot + min(i, rest); };
   const int64_t cs = cta_start(blockIdx.x), ce = cta_start(blockIdx.x + 1);
-  const int64_t ws = cs + (ce - cs) * warp / kDecWarps, we = cs + (ce - cs) * (warp + 1) / kDecWarps;
+  const int64_t ws = cs + (ce - cs) * warp / kWarps, we = cs + (ce - cs) * (warp + 1) / kWarps;
 
   // the pair that holds tile x of the line
   const auto locate = [&](int64_t x) {
     int64_t base = 0;
     DecPair p = {0, 0, 0, 1, 0, 0, 0};
     for (int b0 = 0; b0 < a.s.B; b0 += 32) {
-      const DecPair q = dec_sequence(a, b0 + lane, G, args.max_rows, false);
-      const int64_t n = static_cast<int64_t>(q.tiles) * groups_of(q.n) * a.c.Hkv;
+      const DecPair q = b0 == 0 ? mine : dec_sequence(a, b0 + lane, G, args.max_rows, false);
+      const int64_t n = work_of(q);
       int64_t sum = n;
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
@@ -239,7 +253,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
         p.row0 = __shfl_sync(0xffffffffu, q.row0, src);
         p.n = __shfl_sync(0xffffffffu, q.n, src);
         const int64_t first = base + __shfl_sync(0xffffffffu, sum - n, src);
-        p.j = static_cast<int>((x - first) / p.tiles);
+        // (a sequence's share is under 2^32: at most 4096 pairs of 2^19 tiles)
+        p.j = static_cast<int>(static_cast<uint32_t>(x - first) / static_cast<uint32_t>(p.tiles));
         p.first = first + static_cast<int64_t>(p.j) * p.tiles;
         break;
       }
@@ -271,19 +286,19 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     const int tok0 = static_cast<int>(x_next - nxt.first) * kDecTile;
     ++x_next;
     const int n = min(nxt.len - tok0, kDecTile);
-    const int b0 = tok0 / P;
+    const int b0 = tok0 >> shift;
     if (nxt.b != blk_b || b0 < blk0 || b0 + blocks_per_tile > blk0 + 32) {
       blk_b = nxt.b;
       blk0 = b0;
       const int i = b0 + lane;
-      blk = i < a.c.max_blocks && static_cast<int64_t>(i) * P < nxt.len
+      blk = i < a.c.max_blocks && (static_cast<int64_t>(i) << shift) < nxt.len
                 ? __ldg(a.c.table + static_cast<int64_t>(nxt.b) * a.c.max_blocks + i) : 0;
       if (blk < 0 || blk >= a.c.num_pages) {
         atomicCAS(a.err, 0, kErrKv8Range);
         blk = 0;
       }
     }
-    const int copies = n > 0 ? (n + rows_per_copy - 1) / rows_per_copy : 0;
+    const int copies = n <= 0 ? 0 : n > rows_per_copy ? 2 : 1;
     const int page0 = __shfl_sync(0xffffffffu, blk, b0 - blk0);
     const int page1 = __shfl_sync(0xffffffffu, blk, min(b0 - blk0 + blocks_per_tile - 1, 31));
     const int kvh = nxt.j / groups_of(nxt.n);
@@ -306,7 +321,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     }
   };
 
-  for (int i = 0; i < kDecStages && i < n_mine; ++i) request(i);
+  for (int i = 0; i < kStages && i < n_mine; ++i) request(i);
 
   uint32_t qf[16];             // this lane's column's query, dimensions 32c ..
   float O[8][4], m[2], l[2];   // columns 2c, 2c + 1
@@ -456,8 +471,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
       }
     }
     __syncwarp();  // the stage is read
-    if (it + kDecStages < n_mine) request(stage);
-    if (++stage == kDecStages) {
+    if (it + kStages < n_mine) request(stage);
+    if (++stage == kStages) {
       stage = 0;
       phase ^= 1u;
     }
@@ -498,11 +513,12 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int col = 2 * c + k;
+        if (col >= kCols) continue;
         if (g == 0) {
           part[col] = m[k];
-          part[kDecCols + col] = l[k];
+          part[kCols + col] = l[k];
         }
-        float4* dst = reinterpret_cast<float4*>(part + 2 * kDecCols + col * kKv8D + 16 * g);
+        float4* dst = reinterpret_cast<float4*>(part + 2 * kCols + col * kKv8D + 16 * g);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           dst[i] = make_float4(O[2 * i][k], O[2 * i][k + 2], O[2 * i + 1][k], O[2 * i + 1][k + 2]);
@@ -512,65 +528,95 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
   }
   __syncthreads();
 
-  // ---- partial results of one pair, joined in the order of the line: warp w
-  // takes column w, lane l dimensions 4l .. 4l + 3
-  for (int e = 0; e < 2 * kDecWarps;) {
+  // ---- partial results of one pair, joined in the order of the line: thread
+  // (column, two dimensions)
+  constexpr int kEntries = 2 * kWarps;
+  const int64_t my_first = lane < kEntries ? s_pairs[lane].first : 0;
+  const uint32_t used = __ballot_sync(0xffffffffu, lane < kEntries && s_pairs[lane].b >= 0);
+  const uint32_t before = used & ((1u << lane) - 1u);
+  const int64_t prev_first = __shfl_sync(0xffffffffu, my_first, before != 0 ? 31 - __clz(before) : 0);
+  uint32_t leaders = __ballot_sync(0xffffffffu, ((used >> lane) & 1u) != 0 && (before == 0 || prev_first != my_first));
+  // where a pair that crosses CTAs has its partial result: a CTA has at most
+  // two such pairs, one that begins at or before its start and one after
+  const auto slot_of = [&](const DecPair& p, int i) {
+    return args.part + (2 * i + (p.first <= cta_start(i) ? 0 : 1)) * kDecPart;
+  };
+  int crossing[2] = {-1, -1};  // their first entries
+  while (leaders != 0) {
+    const int e = __ffs(leaders) - 1;
+    leaders &= leaders - 1u;
+    const uint32_t members = used & ~((1u << e) - 1u) & (leaders != 0 ? (leaders & (0u - leaders)) - 1u : 0xffffffffu);
     const DecPair p = s_pairs[e];
-    if (p.b < 0) {
-      ++e;
-      continue;
-    }
     const int groups = groups_of(p.n), r0 = p.j % groups * kDecCols;
     const int nh = min(p.n * G - r0, kDecCols);
-    float m = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (; e < 2 * kDecWarps; ++e) {
-      if (s_pairs[e].b < 0) continue;
-      if (s_pairs[e].first != p.first) break;
-      if (warp < nh) {
-        const float* part = part_of(e);
-        dec_join(m, l, o, part[warp], part[kDecCols + warp],
-                 reinterpret_cast<const float4*>(part + 2 * kDecCols + warp * kKv8D)[lane]);
+    const bool whole = p.first >= cs && p.first + p.tiles <= ce;
+    if (!whole) crossing[crossing[0] >= 0 ? 1 : 0] = e;
+    for (int i = t; i < nh * (kKv8D / 2); i += kWarps * 32) {
+      const int col = i >> 6, d = 2 * (i & 63);
+      float m = -INFINITY, l = 0.0f;
+      float2 o = make_float2(0.0f, 0.0f);
+      for (uint32_t left = members; left != 0; left &= left - 1u)
+        m = fmaxf(m, part_of(__ffs(left) - 1)[col]);
+      for (uint32_t left = members; left != 0; left &= left - 1u) {
+        const float* part = part_of(__ffs(left) - 1);
+        const float f = part[col] == -INFINITY ? 0.0f : ex2(part[col] - m);
+        const float2 v = *reinterpret_cast<const float2*>(part + 2 * kCols + col * kKv8D + d);
+        l = fmaf(part[kCols + col], f, l);
+        o.x = fmaf(v.x, f, o.x);
+        o.y = fmaf(v.y, f, o.y);
       }
-    }
-    uint2* dst = reinterpret_cast<uint2*>(a.out + dec_row(a, p, G, p.j / groups, r0 + min(warp, nh - 1))) + lane;
-    if (p.first >= cs && p.first + p.tiles <= ce) {
-      if (warp < nh) *dst = dec_pack(o, l);
-      continue;
-    }
-    // the pair crosses CTAs
-    const auto owner = [&](int64_t x) { return static_cast<int>(((x + 1) * ctas - 1) / total); };
-    const auto slot_of = [&](int i) { return args.part + (2 * i + (p.first <= cta_start(i) ? 0 : 1)) * kDecPart; };
-    const int first = owner(p.first), last = owner(p.first + p.tiles - 1);
-    if (warp < nh) {
-      float* part = slot_of(static_cast<int>(blockIdx.x));
-      if (lane == 0) {
-        part[warp] = m;
-        part[kDecCols + warp] = l;
-      }
-      reinterpret_cast<float4*>(part + 2 * kDecCols + warp * kKv8D)[lane] = o;
-    }
-    __threadfence();
-    __syncthreads();
-    if (t == 0) *s_last = atom_add_relaxed_gpu(args.count + first, 1) == last - first ? 1 : 0;
-    __syncthreads();
-    if (*s_last) {
-      __threadfence();
-      if (warp < nh) {
-        m = -INFINITY;
-        l = 0.0f;
-        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int i = first; i <= last; ++i) {
-          const float* part = slot_of(i);
-          dec_join(m, l, o, __ldcg(part + warp), __ldcg(part + kDecCols + warp),
-                   __ldcg(reinterpret_cast<const float4*>(part + 2 * kDecCols + warp * kKv8D) + lane));
+      if (whole) {
+        *reinterpret_cast<__half2*>(a.out + dec_row(a, p, G, p.j / groups, r0 + col) + d) = dec_pack(o, l);
+      } else {
+        float* part = slot_of(p, static_cast<int>(blockIdx.x));
+        if (d == 0) {
+          part[col] = m;
+          part[kDecCols + col] = l;
         }
-        *dst = dec_pack(o, l);
+        *reinterpret_cast<float2*>(part + 2 * kDecCols + col * kKv8D + d) = o;
       }
-      if (t == 0) args.count[first] = 0;
     }
-    __syncthreads();  // s_last is read
+  }
+  if (crossing[0] < 0) return;
+  // pairs that cross CTAs: the last one to arrive joins them. (Both of a CTA's
+  // arrivals together: each step costs a round trip to L2.)
+  const auto owner = [&](int64_t x) {
+    const int64_t longer = rest * (quot + 1);
+    return static_cast<int>(x < longer ? x / (quot + 1) : rest + (x - longer) / quot);
+  };
+  __threadfence();
+  __syncthreads();
+  if (t < 2) {
+    int last = 0;
+    const int e = t == 0 ? crossing[0] : crossing[1];
+    if (e >= 0) {
+      const int c0 = owner(s_pairs[e].first), c1 = owner(s_pairs[e].first + s_pairs[e].tiles - 1);
+      last = atom_add_relaxed_gpu(args.count + c0, 1) == c1 - c0 ? 1 : 0;
+    }
+    s_last[t] = last;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    if (!s_last[k]) continue;
+    __threadfence();
+    const DecPair p = s_pairs[k == 0 ? crossing[0] : crossing[1]];
+    const int groups = groups_of(p.n), r0 = p.j % groups * kDecCols;
+    const int nh = min(p.n * G - r0, kDecCols);
+    const int c0 = owner(p.first), c1 = owner(p.first + p.tiles - 1);
+    for (int i = t; i < nh * (kKv8D / 2); i += kWarps * 32) {
+      const int col = i >> 6, d = 2 * (i & 63);
+      float m = -INFINITY, l = 0.0f;
+      float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+      for (int n = c0; n <= c1; ++n) {
+        const float* part = slot_of(p, n);
+        dec_join(m, l, o, __ldcg(part + col), __ldcg(part + kDecCols + col),
+                 __ldcg(reinterpret_cast<const float2*>(part + 2 * kDecCols + col * kKv8D + d)));
+      }
+      *reinterpret_cast<__half2*>(a.out + dec_row(a, p, G, p.j / groups, r0 + col) + d) = dec_pack(o, l);
+    }
+    if (t == 0) args.count[c0] = 0;
   }
 }
 

@@ -84,13 +84,14 @@ w4a8_status_t launch_kv8_decode(const CUtensorMap& map, const Kv8DecodeArgs& d, 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return launch_status();
   if (!done[dev]) {
-    if (cudaFuncSetAttribute(kv8_decode_kernel<DUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecSmem::kBytes) !=
+    if (cudaFuncSetAttribute(kv8_decode_kernel<DUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             DecCfg<DUP>::kBytes) !=
         cudaSuccess)
       return launch_status();
     done[dev] = true;
   }
-  return launch_pdl(kv8_decode_kernel<DUP>, dim3(static_cast<unsigned>(grid)), dim3(kDecWarps * 32), DecSmem::kBytes,
-                    stream, 1, map, d);
+  return launch_pdl(kv8_decode_kernel<DUP>, dim3(static_cast<unsigned>(grid)), dim3(DecCfg<DUP>::kWarps * 32),
+                    DecCfg<DUP>::kBytes, stream, 1, map, d);
 }
 
 // Sequences whose rows (new tokens times query heads per kv head) are at most
@@ -111,8 +112,7 @@ w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_c
   // one CTA per SM, no more than the longest possible batch has tiles for
   const int64_t tiles = (c->max_blocks * c->page + kDecTile - 1) / kDecTile * a.s.B * a.c.Hkv *
                         ((d.max_rows + kDecCols - 1) / kDecCols);
-  int64_t grid = (tiles + kDecWarps - 1) / kDecWarps;
-  if (grid > dev->sms) grid = dev->sms;
+  int64_t grid = tiles < dev->sms ? tiles : dev->sms;
   if (grid > kDecMaxCtas) grid = kDecMaxCtas;
   if (d.max_rows <= 4) return launch_kv8_decode<true>(map, d, static_cast<int>(grid), stream);
   return launch_kv8_decode<false>(map, d, static_cast<int>(grid), stream);
