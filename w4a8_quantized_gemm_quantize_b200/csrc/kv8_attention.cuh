@@ -105,15 +105,15 @@ constexpr int kDecCols = 8;
 constexpr int kDecPart = kDecCols * (2 + kKv8D);  // floats of a partial result in the workspace: m[8], l[8], O[8][128]
 constexpr int kDecMaxCtas = 256;
 
-// One CTA per SM. Up to four columns (DUP): 12 warps with two stages each
-// (measured, 16 sequences of 2048 to 4096 tokens, 8 kv heads: 8 warps with three
-// stages XX us, 12 with two XX us: the warps wait for their own chains of
-// instructions, not for the copies); up to eight: 10 warps, whose partial
-// results take twice the room.
+// One CTA per SM. Up to four columns (DUP): 12 warps with two stages each (8
+// sequences of 2048 to 4096 tokens, 64 kv heads: 75 us, with 8 warps of three
+// stages 81: the warps wait for their own chains of instructions more than for
+// the copies). Up to eight, whose partial results take twice the room: 8 warps
+// with three (16 sequences, 8 query heads a kv head: 37 us, with 10 of two 40).
 template <bool DUP>
 struct DecCfg {
-  static constexpr int kWarps = DUP ? 12 : 10;
-  static constexpr int kStages = 2;
+  static constexpr int kWarps = DUP ? 12 : 8;
+  static constexpr int kStages = DUP ? 2 : 3;
   static constexpr int kCols = DUP ? 4 : kDecCols;
   static constexpr int kRingBytes = kStages * kDecStageBytes;
   static constexpr int kPartBytes = kCols * (2 + kKv8D) * 4;  // m[], l[], O[][128]
@@ -222,8 +222,16 @@ __global__ void __launch_bounds__(DecCfg<DUP>::kWarps * 32, 1)
     total += work_of(dec_sequence(a, b, G, args.max_rows, blockIdx.x == 0 && warp == 0));
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (total == 0) return;
-  const int64_t want = (total + kWarps - 1) / kWarps;
-  const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
+  // CTAs: a tile a warp at least; where that is fewer than there are, as many
+  // for each pair, so that pairs of one length end with a CTA (joining across
+  // CTAs costs 3 us of a call of 10)
+  int ctas = gridDim.x;
+  if (total < static_cast<int64_t>(kWarps) * ctas) {
+    int pairs = mine.tiles > 0 ? groups_of(mine.n) * a.c.Hkv : 0;
+    for (int o = 16; o > 0; o >>= 1) pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
+    const int want = (static_cast<int>(total) + kWarps - 1) / kWarps;
+    ctas = a.s.B <= 32 && pairs <= static_cast<int>(gridDim.x) ? pairs * max(want / pairs, 1) : want;
+  }
   if (static_cast<int>(blockIdx.x) >= ctas) return;
   // CTA i takes quot tiles, one more if i < rest
   const int64_t quot = total / ctas;

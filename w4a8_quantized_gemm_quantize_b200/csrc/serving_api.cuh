@@ -95,8 +95,17 @@ w4a8_status_t launch_kv8_decode(const CUtensorMap& map, const Kv8DecodeArgs& d, 
 }
 
 // Sequences whose rows (new tokens times query heads per kv head) are at most
-// this many go to the decode kernel, others to the prefill kernel.
-constexpr int kKv8FewRows = 32;
+// this many go to the decode kernel, others to the prefill kernel. The decode
+// kernel takes 0.25 us an SM for 8 rows and 32 tokens, spread over all SMs; the
+// prefill kernel 2.3 us for 256 rows and 128 tokens, on one SM for each
+// (sequence, kv head): equal at 2700 / (B Hkv) rows while those are fewer than
+// the SMs, at 18 beyond. (Measured over 4000 cached tokens, 8 kv heads: 8
+// sequences of 64 rows 120 us in the one, 83 in the other; 1 of 256 rows 65
+// against 85.)
+int kv8_few_rows(int64_t B, int64_t Hkv) {
+  const int64_t n = 2700 / (B * Hkv);
+  return static_cast<int>(n < 18 ? 18 : n > 256 ? 256 : n);
+}
 
 w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_cache_t* c, void* workspace,
                          cudaStream_t stream) {
@@ -108,7 +117,7 @@ w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_c
   d.a = a;
   d.count = static_cast<int*>(workspace);
   d.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kDecMaxCtas * 4);
-  d.max_rows = a.s.q_start == nullptr ? G : kKv8FewRows;
+  d.max_rows = a.s.q_start == nullptr ? G : kv8_few_rows(a.s.B, a.c.Hkv);
   // one CTA per SM, no more than the longest possible batch has tiles for
   const int64_t tiles = (c->max_blocks * c->page + kDecTile - 1) / kDecTile * a.s.B * a.c.Hkv *
                         ((d.max_rows + kDecCols - 1) / kDecCols);
@@ -161,10 +170,11 @@ w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int3
   // each kernel takes the sequences that suit it; one whose share must be
   // empty is not launched
   const int64_t rows = T * (Hq / c->Hkv);
-  if (rows <= kKv8FewRows) return kv8_decode(a, dev, c, workspace, stream);
+  const int few = kv8_few_rows(B, c->Hkv);
+  if (rows <= few) return kv8_decode(a, dev, c, workspace, stream);
   if (B == 1) return kv8_prefill(a, 0, stream);
   st = kv8_decode(a, dev, c, workspace, stream);
-  return st != W4A8_OK ? st : kv8_prefill(a, kKv8FewRows, stream);
+  return st != W4A8_OK ? st : kv8_prefill(a, few, stream);
 }
 
 }  // namespace
