@@ -4,7 +4,7 @@
 // rstd = 1 / sqrt(mean(h^2) + eps) (fp32, IEEE square root and divide), then
 // the per-token quantization of quantize_act.cuh on the fp32 values of y (no
 // rounding to fp16 in between): sA = fp16_rn(max |y| / 127), A8 =
-// clamp(rint(y / sA), -127, 127), rowsum = sum A8. What w4a8_gemm takes, so
+// clamp(rint(y * (1 / sA)), -127, 127), rowsum = sum A8. What w4a8_gemm takes, so
 // that the norm in front of a linear layer ("QServe/QoQ" abstract: W4A8
 // serving) costs one read of its input instead of a write and two reads more.
 //
@@ -36,7 +36,19 @@ __device__ __forceinline__ float block_all(float v, float* red) {
   return v;
 }
 
-// VPT: 16-byte vectors (8 halves) per thread; K <= THREADS * VPT * 8.
+// Codes of four values in units of the scale, |v * inv| < 2^21: rint of the
+// exact product (ties to even) by one fused multiply-add into the unit range of
+// 1.5 * 2^23, whose low byte is then the code.
+__device__ __forceinline__ uint32_t pack_codes(const float* v, float inv) {
+  constexpr float kMagic = 12582912.0f;
+  const uint32_t c0 = __float_as_uint(fmaf(v[0], inv, kMagic)), c1 = __float_as_uint(fmaf(v[1], inv, kMagic));
+  const uint32_t c2 = __float_as_uint(fmaf(v[2], inv, kMagic)), c3 = __float_as_uint(fmaf(v[3], inv, kMagic));
+  return __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
+}
+
+// VPT: 16-byte vectors (8 halves) per thread; K <= THREADS * VPT * 8. KEEP: the
+// weights and y stay in registers too; with 8 vectors a thread only the row does
+// (64 registers a thread at 1024 threads), and y is worked out twice.
 template <int THREADS, int VPT, bool RES>
 __global__ void __launch_bounds__(THREADS) rmsnorm_quantize_kernel(const __half* X, const __half* R,
                                                                    const __half* __restrict__ W, float eps,
@@ -53,24 +65,39 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_quantize_kernel(const __half*
   const uint4* x = reinterpret_cast<const uint4*>(X + m * K);
   const uint4* r = reinterpret_cast<const uint4*>(R + m * K);
   const uint4* w = reinterpret_cast<const uint4*>(W);
-  uint4 v[VPT];
+  constexpr bool KEEP = VPT <= 4;
+  constexpr int kKeep = KEEP ? VPT : 1;
+  uint4 v[VPT], rv[kKeep], wv[kKeep];
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {  // every read of the row under way at once
+      const int idx = threadIdx.x + i * THREADS;
+      v[i] = rv[i] = wv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (idx < nvec) {
+        v[i] = __ldcs(x + idx);
+        if constexpr (RES) rv[i] = __ldcs(r + idx);
+        wv[i] = __ldg(w + idx);
+      }
+    }
+  }
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int idx = threadIdx.x + i * THREADS;
-    v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (idx < nvec) {
-      v[i] = x[idx];
-      if constexpr (RES) {
-        const uint4 rv = r[idx];
-        __half2* a = reinterpret_cast<__half2*>(&v[i]);
-        const __half2* b = reinterpret_cast<const __half2*>(&rv);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = __hadd2_rn(a[j], b[j]);  // one rounding of the exact sum
-        reinterpret_cast<uint4*>(H + m * K)[idx] = v[i];
-      }
+    uint4 rr = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (KEEP) {
+      rr = rv[i];
+    } else {
+      v[i] = idx < nvec ? __ldcs(x + idx) : rr;
+      if (RES && idx < nvec) rr = __ldcs(r + idx);
     }
-    const __half2* h = reinterpret_cast<const __half2*>(&v[i]);
+    __half2* h = reinterpret_cast<__half2*>(&v[i]);
+    if constexpr (RES) {
+      const __half2* b = reinterpret_cast<const __half2*>(&rr);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = __hadd2_rn(h[j], b[j]);  // one rounding of the exact sum
+      if (idx < nvec) reinterpret_cast<uint4*>(H + m * K)[idx] = v[i];
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = __half22float2(h[j]);
@@ -80,50 +107,70 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_quantize_kernel(const __half*
   }
   sum = block_all<THREADS, false>(sum, s_sum);
   const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(K)), eps)));
+  const auto norm_of = [&](int i, float (&y)[8]) {
+    const int idx = threadIdx.x + i * THREADS;
+    uint4 ww = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (KEEP) {
+      ww = wv[i];
+    } else if (idx < nvec) {
+      ww = __ldg(w + idx);
+    }
+    const __half2* h = reinterpret_cast<const __half2*>(&v[i]);
+    const __half2* g = reinterpret_cast<const __half2*>(&ww);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(h[j]), q = __half22float2(g[j]);
+      y[2 * j] = f.x * rstd * q.x;
+      y[2 * j + 1] = f.y * rstd * q.y;
+    }
+  };
+  float y[kKeep][8];
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int idx = threadIdx.x + i * THREADS;
-    if (idx < nvec) {
-      const uint4 wv = __ldg(w + idx);
-      const __half2* h = reinterpret_cast<const __half2*>(&v[i]);
-      const __half2* g = reinterpret_cast<const __half2*>(&wv);
+    float(&yy)[8] = y[KEEP ? i : 0];
+    norm_of(i, yy);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(h[j]), q = __half22float2(g[j]);
-        amax = fmaxf(amax, fmaxf(fabsf(f.x * rstd * q.x), fabsf(f.y * rstd * q.y)));
-      }
-    }
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(yy[e]));
   }
   amax = block_all<THREADS, true>(amax, s_max);
   const __half s_h = __float2half_rn(__fdiv_rn(amax, 127.0f));
   const float sf = __half2float(s_h);
+  const float inv = sf > 0.0f ? __fdiv_rn(1.0f, sf) : 0.0f;
+  // A normal scale is within 2^-11 of amax / 127, so that no code passes 127;
+  // a subnormal one may be half of it.
+  const bool clamp = sf < 6.2e-5f;
+  const float top = 127.0f * sf;
   int local = 0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int idx = threadIdx.x + i * THREADS;
-    if (idx < nvec) {
-      const uint4 wv = __ldg(w + idx);
-      const __half2* h = reinterpret_cast<const __half2*>(&v[i]);
-      const __half2* g = reinterpret_cast<const __half2*>(&wv);
-      int q[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (sf != 0.0f) {
+    float(&yy)[8] = y[KEEP ? i : 0];
+    if constexpr (!KEEP) norm_of(i, yy);
+    if (clamp) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = __half22float2(h[j]), u = __half22float2(g[j]);
-          q[2 * j] = quant_code<127>(f.x * rstd * u.x, sf);
-          q[2 * j + 1] = quant_code<127>(f.y * rstd * u.y, sf);
-          local += q[2 * j] + q[2 * j + 1];
-        }
-      }
-      CodeOut<8>::store(A8 + m * K, idx, q);
+      for (int e = 0; e < 8; ++e) yy[e] = fminf(fmaxf(yy[e], -top), top);
+    }
+    if (idx < nvec) {
+      const uint2 c = make_uint2(pack_codes(yy, inv), pack_codes(yy + 4, inv));
+      reinterpret_cast<uint2*>(A8 + m * K)[idx] = c;
+      local = __dp4a(static_cast<int>(c.x), 0x01010101, local);
+      local = __dp4a(static_cast<int>(c.y), 0x01010101, local);
     }
   }
-  if (rowsum != nullptr) {
-    const int total = block_sum<THREADS>(local, s_cnt);
-    if (threadIdx.x == 0) rowsum[m] = total;
-  }
   if (threadIdx.x == 0) sA[m] = s_h;
+  if (rowsum != nullptr) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) local += __shfl_xor_sync(0xffffffffu, local, o);
+    if ((threadIdx.x & 31) == 0) s_cnt[threadIdx.x >> 5] = local;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      local = threadIdx.x < THREADS / 32 ? s_cnt[threadIdx.x] : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) local += __shfl_xor_sync(0xffffffffu, local, o);
+      if (threadIdx.x == 0) rowsum[m] = local;
+    }
+  }
 }
 
 }  // namespace w4a8
