@@ -183,14 +183,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
   const int b = kv8_find(a.s, slot, G, 2 * kPreRows, 1);
   if (b < 0) return;
   const Kv8Seq sq = kv8_sequence(a.s, b, static_cast<int64_t>(a.c.max_blocks) * P, t == 0 ? a.err : nullptr);
-  const int first = sq.first, n = kv8_row_start(a.s, b + 1) - first;
-  const int64_t row0 = static_cast<int64_t>(slot - (static_cast<int64_t>(first) * G / (2 * kPreRows) + b)) * 2 * kPreRows;
-  const int64_t rows = static_cast<int64_t>(n) * G;
+  // (rows times heads of a batch are under 2^31)
+  const int first = sq.first, rows = (kv8_row_start(a.s, b + 1) - first) * G;
+  const int row0 = (slot - static_cast<int>(static_cast<int64_t>(first) * G / (2 * kPreRows)) - b) * 2 * kPreRows;
   if (row0 >= rows || rows <= few_rows) return;  // (few rows: the decode kernel's)
   if (sq.n < 0) {  // a length that does not fit (reported): zeros
-    const int64_t r = row0 + t;
+    const int r = row0 + t;
     if (t < 2 * kPreRows && r < rows) {
-      uint4* dst = reinterpret_cast<uint4*>(a.out + ((first + r / G) * a.Hq + kvh * G + r % G) * kKv8D);
+      uint4* dst = reinterpret_cast<uint4*>(a.out + ((static_cast<int64_t>(first) + r / G) * a.Hq + kvh * G + r % G) * kKv8D);
       for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
     }
     return;
@@ -199,8 +199,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
   int nt[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int64_t last = min(row0 + (k + 1) * kPreRows, rows) - 1;  // its last row
-    nt[k] = last < row0 + k * kPreRows ? 0 : (sq.pos0 + static_cast<int>(last / G) + kPreTile) / kPreTile;
+    const int last = min(row0 + (k + 1) * kPreRows, rows) - 1;  // its last row
+    nt[k] = last < row0 + k * kPreRows ? 0 : (sq.pos0 + last / G + kPreTile) / kPreTile;
   }
   const int tiles = max(nt[0], nt[1]);
 
@@ -224,10 +224,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
     fence_barrier_init();
     s_tmem[1] = 0u;  // set by the first wait that gives up
   }
-  if (warp == 24) {
-    tmem_alloc(s_tmem, kPreTmemCols);
-    tmem_relinquish();
-  }
   const uint32_t bar0 = smem_u32(bars), abort = smem_u32(s_tmem + 1);
   const auto wait = [&](int bar, int phase) {
     return bar_wait<false>(bar0 + 8 * bar, static_cast<uint32_t>(phase) & 1u, abort, a.err);
@@ -239,39 +235,40 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
     return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
   };
 
-  // this softmax thread's row, and its half of the query into shared memory
-  const int blk = warp >> 3, half = (warp >> 2) & 1;  // block of rows, half of the columns (softmax warps)
-  const int lr = (warp & 3) * 32 + lane;              // row of the block, TMEM lane
-  const int64_t row = row0 + blk * kPreRows + lr;
-  const bool mine = warp < 16 && row < rows;
-  // where its half row lies in q and out; -1: no row
-  const int64_t at =
-      mine ? ((static_cast<int64_t>(first) + row / G) * a.Hq + kvh * G + row % G) * kKv8D + 64 * half : -1;
-  const int limit = mine ? sq.pos0 + static_cast<int>(row / G) + 1 : 1;
-  if (warp < 16) {
-    uint8_t* dst = sm + PreSmem::kOffQ + blk * PreSmem::kOperand + half * PreSmem::kBlock + lr * 128;
-    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;  // scores are taken with |scale|
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (mine) {
-        v = __ldg(reinterpret_cast<const uint4*>(a.q + at) + i);
-        v.x ^= flip;
-        v.y ^= flip;
-        v.z ^= flip;
-        v.w ^= flip;
-      }
-      *reinterpret_cast<uint4*>(dst + ((i ^ (lr & 7)) << 4)) = v;
-    }
-    fence_proxy_async_smem();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  // barriers, queries and the tensor memory's address are there: every role
+  // comes here once, after what it can request before
+  const auto set_up = [&]() {
+    tc_fence_before();
+    named_bar_sync(1, kPreThreads);
+    tc_fence_after();
+    return *s_tmem;
+  };
 
   if (warp < 16) {
     // ------------------------------------------------------------ softmax
+    // this thread's row, and its half of the query into shared memory
+    const int blk = warp >> 3, half = (warp >> 2) & 1;  // block of rows, half of the columns
+    const int lr = (warp & 3) * 32 + lane;              // row of the block, TMEM lane
+    const int row = row0 + blk * kPreRows + lr;
+    const bool mine = row < rows;
+    const int ti = mine ? row / G : 0;
+    // where its half row lies in q and out; -1: no row
+    const int64_t at =
+        mine ? ((static_cast<int64_t>(first) + ti) * a.Hq + kvh * G + (row - ti * G)) * kKv8D + 64 * half : -1;
+    const int limit = mine ? sq.pos0 + ti + 1 : 1;
+    {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = mine ? __ldg(reinterpret_cast<const uint4*>(a.q + at) + i) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t dst = smem_u32(sm) + PreSmem::kOffQ + blk * PreSmem::kOperand + half * PreSmem::kBlock + lr * 128;
+      const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;  // scores are taken with |scale|
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        st_shared_16(dst + ((i ^ (lr & 7)) << 4), v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+    }
+    fence_proxy_async_smem();
+    const uint32_t tmem = set_up();
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPreRegsSoftmax));
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     // this thread's half of its row of S, P and O
@@ -390,7 +387,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
       }
     }
   } else if (warp < 24) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPreRegsBytes));
     // ---------------------------------------------------- bytes to operands
     const int kv = warp >= 20 ? 1 : 0;
     // a pass covers 16 tokens: lanes in pairs of rows and quarters of 64 bytes,
@@ -430,6 +426,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
 #pragma unroll
     for (int i = 0; i < 8; ++i) load(i, places0);
     int page = page_of(1);
+    set_up();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPreRegsBytes));
     for (int j = 0; j < tiles; ++j) {
       const int next = place_of(j + 1, page);
       page = page_of(j + 2);
@@ -454,6 +452,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
       for (int i = 0; i < 8; ++i) load(i, next);
     }
   } else {
+    if (warp == 24) {
+      tmem_alloc(s_tmem, kPreTmemCols);
+      tmem_relinquish();
+    }
+    const uint32_t tmem = set_up();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPreRegsIssue));
     // ----------------------------------------------------------- products
     // (a descriptor's address is in units of 16 bytes in its low bits)
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
   __syncthreads();
   if (warp == 24) {
     tc_fence_after();
-    tmem_dealloc(tmem, kPreTmemCols);
+    tmem_dealloc(*s_tmem, kPreTmemCols);
   }
 }
 

@@ -200,7 +200,7 @@ w4a8_status_t w4a8_rmsnorm_quantize_act(const void* X, const void* residual, con
   if (nvec <= 256) return launch_rmsnorm<256, 1>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
   if (nvec <= 512) return launch_rmsnorm<256, 2>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
   if (nvec <= 1024) return launch_rmsnorm<256, 4>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
-  if (nvec <= 2048) return launch_rmsnorm<512, 4>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
+  if (nvec <= 2048) return launch_rmsnorm<256, 8>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
   if (nvec <= 4096) return launch_rmsnorm<1024, 4>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
   return launch_rmsnorm<1024, 8>(x, r, w, eps, M, K, h, A8, s, rowsum, cs);
 }
