@@ -311,6 +311,18 @@ def test_prefill_many_sequences():
     check_attention(c, attend(c, False), 2.0 ** -11)
 
 
+@pytest.mark.parametrize("Hq,Hkv,n,old", [(4, 1, 300, 5000), (8, 8, 260, 3000), (32, 2, 130, 1500), (3, 1, 1000, 500)])
+def test_prefill_cut_into_parts(Hq, Hkv, n, old):
+    """A chunk over a long context: each piece of 256 rows cut over many CTAs and joined; an odd
+    group, rows behind the sequence, a workspace full of garbage behind its counters."""
+    c = case(Hq, Hkv, 32, [n, 0, 19], [old, 40, 700], 500 + n, pad_rows=3)
+    ws = torch.full((w4a8.kv8_workspace_bytes(3, n + 22, Hq, Hkv),), 0x7F, dtype=torch.uint8, device=DEV)
+    ws[:4096] = 0
+    y = attend(c, False, ws)
+    check_attention(c, y, 2.0 ** -11, heads=(0, Hq - 1))
+    assert np.array_equal(y.view(np.uint16), attend(c, False, ws).view(np.uint16))
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(4, 1), (32, 8), (6, 6), (12, 1)])
 def test_prefill_few_and_many_rows_together(Hq, Hkv):
     """Sequences of a few rows beside long chunks, ragged limits that end a tile early, padding rows behind."""
@@ -332,7 +344,8 @@ def test_prefill_of_single_tokens_is_decode():
 def test_attention_repeats_bit_for_bit_and_leaves_the_workspace_clean():
     c = case(32, 8, 64, [1] * 4, [3000, 1, 700, 1023], 24)
     g = [dev(a) for a in c]
-    ws = torch.zeros(w4a8.kv8_workspace_bytes(4, 4, 32, 8), dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(max(w4a8.kv8_workspace_bytes(4, 4, 32, 8), w4a8.kv8_workspace_bytes(3, 247, 8, 2)),
+                     dtype=torch.uint8, device=DEV)
     ref = dev(attend(c, True, ws)).view(torch.int16)
     out = torch.empty_like(g[0])
     bad = torch.zeros((), dtype=torch.int64, device=DEV)

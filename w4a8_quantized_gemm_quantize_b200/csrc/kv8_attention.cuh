@@ -261,8 +261,9 @@ __global__ void __launch_bounds__(DecCfg<DUP>::kWarps * 32, 1)
         p.row0 = __shfl_sync(0xffffffffu, q.row0, src);
         p.n = __shfl_sync(0xffffffffu, q.n, src);
         const int64_t first = base + __shfl_sync(0xffffffffu, sum - n, src);
-        // (a sequence's share is under 2^32: at most 4096 pairs of 2^19 tiles)
-        p.j = static_cast<int>(static_cast<uint32_t>(x - first) / static_cast<uint32_t>(p.tiles));
+        const int64_t in_sequence = x - first;
+        p.j = in_sequence >> 32 ? static_cast<int>(in_sequence / p.tiles)
+                                : static_cast<int>(static_cast<uint32_t>(in_sequence) / static_cast<uint32_t>(p.tiles));
         p.first = first + static_cast<int64_t>(p.j) * p.tiles;
         break;
       }

@@ -29,6 +29,10 @@ namespace w4a8 {
 // own reads of it (1536 of 2048 cycles a tile) leave room for little more than
 // the converted tiles.
 //
+// Few pieces (a chunk of one long prompt): each piece's tiles are cut into
+// `splits` parts on as many CTAs, whose unnormalized outputs, references and sums
+// a second kernel joins.
+//
 // Softmax weights carry their page's value scale, as in the decode kernel: z_j
 // = x_j + log2 sV_j, w_j = 2^(z_j - M + 10), rounded once to fp16 for the
 // product (relative 2^-11; at most 2^15); the denominator sums w_j / sV_j of
@@ -41,6 +45,7 @@ constexpr int kPreThreads = 28 * 32;  // (warp 27 only fills its group of four)
 constexpr int kPreRegs = 72, kPreRegsSoftmax = 88, kPreRegsBytes = 56, kPreRegsIssue = 40;
 static_assert(16 * kPreRegsSoftmax + 8 * kPreRegsBytes + 4 * kPreRegsIssue <= 28 * kPreRegs,
               "setmaxnreg draws on the launch's registers");
+constexpr int kPreMinTiles = 4;    // of a split
 constexpr float kPreShift = 10.0f, kPreSlack = 5.0f;
 
 struct PreSmem {
@@ -164,7 +169,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs a, int slots, int few_rows) {
+struct Kv8PrefillArgs {
+  Kv8AttnArgs a;
+  int slots, few_rows, splits;
+  // splits > 1: [slots * Hkv][splits][256] rows of 128 outputs, then of (reference, sum)
+  float* part;
+  float* part_ml;
+};
+__device__ __forceinline__ int pre_chunk(int tiles, int splits) {
+  return max((tiles + splits - 1) / splits, kPreMinTiles);
+}
+
+// CUT: pieces are cut (an instantiation of its own: what it keeps in registers
+// costs the other 15%).
+template <bool CUT>
+__global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8PrefillArgs args) {
+  const Kv8AttnArgs a = args.a;
   extern __shared__ __align__(1024) uint8_t pre_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pre_smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + PreSmem::kOffBars);
@@ -178,18 +198,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
   grid_launch_dependents();
   // this CTA's rows: slot start_b G / 256 + b + k holds rows 256 k .. of
   // sequence b. Later slots see more of the cache: taken first.
-  const int kvh = static_cast<int>(blockIdx.x) % a.c.Hkv;
-  const int slot = slots - 1 - static_cast<int>(blockIdx.x) / a.c.Hkv;
+  const int split = CUT ? static_cast<int>(blockIdx.x) % args.splits : 0;
+  const int piece = CUT ? static_cast<int>(blockIdx.x) / args.splits : static_cast<int>(blockIdx.x);
+  const int kvh = piece % a.c.Hkv;
+  const int slot = args.slots - 1 - piece / a.c.Hkv;
   const int b = kv8_find(a.s, slot, G, 2 * kPreRows, 1);
   if (b < 0) return;
   const Kv8Seq sq = kv8_sequence(a.s, b, static_cast<int64_t>(a.c.max_blocks) * P, t == 0 ? a.err : nullptr);
   // (rows times heads of a batch are under 2^31)
   const int first = sq.first, rows = (kv8_row_start(a.s, b + 1) - first) * G;
   const int row0 = (slot - static_cast<int>(static_cast<int64_t>(first) * G / (2 * kPreRows)) - b) * 2 * kPreRows;
-  if (row0 >= rows || rows <= few_rows) return;  // (few rows: the decode kernel's)
+  if (row0 >= rows || rows <= args.few_rows) return;  // (few rows: the decode kernel's)
   if (sq.n < 0) {  // a length that does not fit (reported): zeros
     const int r = row0 + t;
-    if (t < 2 * kPreRows && r < rows) {
+    if (split == 0 && t < 2 * kPreRows && r < rows) {
       uint4* dst = reinterpret_cast<uint4*>(a.out + ((static_cast<int64_t>(first) + r / G) * a.Hq + kvh * G + r % G) * kKv8D);
       for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -202,7 +224,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
     const int last = min(row0 + (k + 1) * kPreRows, rows) - 1;  // its last row
     nt[k] = last < row0 + k * kPreRows ? 0 : (sq.pos0 + last / G + kPreTile) / kPreTile;
   }
-  const int tiles = max(nt[0], nt[1]);
+  // this CTA's part of them: `tiles` from tile0 on
+  int tile0 = 0, tiles = max(nt[0], nt[1]);
+  bool whole = true;
+  if constexpr (CUT) {
+    const int chunk = pre_chunk(tiles, args.splits);
+    whole = chunk >= tiles;
+    tile0 = split * chunk;
+    tiles = min(tiles - tile0, chunk);
+    if (tiles <= 0) return;
+    nt[0] = max(min(nt[0] - tile0, tiles), 0);
+    nt[1] = max(min(nt[1] - tile0, tiles), 0);
+  }
 
   if (t == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -255,7 +288,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
     // where its half row lies in q and out; -1: no row
     const int64_t at =
         mine ? ((static_cast<int64_t>(first) + ti) * a.Hq + kvh * G + (row - ti * G)) * kKv8D + 64 * half : -1;
-    const int limit = mine ? sq.pos0 + ti + 1 : 1;
+    const int limit = (mine ? sq.pos0 + ti + 1 : 1) - tile0 * kPreTile;  // tokens that it sees, from tile0 on
     {
       uint4 v[8];
 #pragma unroll
@@ -368,11 +401,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
       give(mine_nt, l);
       l += take(mine_nt, ok);
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const int64_t part_row =
+          ((static_cast<int64_t>(slot) * a.c.Hkv + kvh) * args.splits + split) * (2 * kPreRows) + blk * kPreRows + lr;
+      if (CUT && !whole && half == 0) *reinterpret_cast<float2*>(args.part_ml + 2 * part_row) = make_float2(ref, l);
 #pragma unroll 1
       for (int q = 0; q < 2; ++q) {
         uint32_t r[32];
         tmem_ld_32_wait(tO + 32 * q, r);
-        if (at >= 0) {
+        if (CUT && !whole) {
+          float4* dst = reinterpret_cast<float4*>(args.part + part_row * kKv8D + 64 * half + 32 * q);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]),
+                                 __uint_as_float(r[4 * i + 3]));
+        } else if (at >= 0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint4 y;
@@ -398,12 +440,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
     // lane i < 8: the page of pass i of tile j, -1 behind the sequence's end;
     // requested two tiles ahead of the codes' use
     const auto page_of = [&](int j) {
-      const int tok = j * kPreTile + 16 * (lane & 7);
+      const int tok = (tile0 + j) * kPreTile + 16 * (lane & 7);
       return tok < sq.len && j < tiles ? __ldg(table + (tok >> shift)) : -1;
     };
     // where the pass begins, as a row of 128 bytes of the cache
     const auto place_of = [&](int j, int page) {
-      const int tok = j * kPreTile + 16 * (lane & 7);
+      const int tok = (tile0 + j) * kPreTile + 16 * (lane & 7);
       if (tok >= sq.len || j >= tiles) return -1;
       if (page < 0 || page >= a.c.num_pages) {
         atomicCAS(a.err, 0, kErrKv8Range);
@@ -515,7 +557,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
       // the scales of a tile's passes of 16 tokens (lane i < 8: of pass i)
       const int32_t* table = a.c.table + static_cast<int64_t>(b) * a.c.max_blocks;
       for (int j = 0; j < tiles; ++j) {
-        const int tok = j * kPreTile + 16 * (lane & 7);
+        const int tok = (tile0 + j) * kPreTile + 16 * (lane & 7);
         float sk = 0.0f, sv = 1.0f;
         if (tok < sq.len) {
           const int page = min(max(__ldg(table + tok / P), 0), a.c.num_pages - 1);  // (reported where the codes are read)
@@ -544,6 +586,51 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8AttnArgs
     tc_fence_after();
     tmem_dealloc(*s_tmem, kPreTmemCols);
   }
+}
+
+// Joins the parts of cut pieces: a warp for each (row of the batch, query
+// head), lane l dimensions 4 l .. 4 l + 3, in the order of the parts.
+constexpr int kPreJoinWarps = 8;
+__global__ void __launch_bounds__(kPreJoinWarps * 32) kv8_prefill_join_kernel(const __grid_constant__ Kv8PrefillArgs args) {
+  const Kv8AttnArgs& a = args.a;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, G = a.Hq / a.c.Hkv;
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * kPreJoinWarps + (threadIdx.x >> 5);
+  if (x >= static_cast<int64_t>(a.s.T) * a.Hq) return;
+  const int batch_row = static_cast<int>(x / a.Hq), h = static_cast<int>(x % a.Hq);
+  const int b = kv8_find(a.s, batch_row, 1, 1, 0);
+  if (b < 0) return;
+  const Kv8Seq sq = kv8_sequence(a.s, b, static_cast<int64_t>(a.c.max_blocks) * a.c.P, nullptr);
+  const int n = kv8_row_start(a.s, b + 1) - sq.first, ti = batch_row - sq.first;
+  if (ti >= n || sq.n < 0 || n * G <= args.few_rows) return;
+  const int kvh = h / G, row = ti * G + h % G, piece_row0 = row / (2 * kPreRows) * (2 * kPreRows);
+  const int slot = static_cast<int>(static_cast<int64_t>(sq.first) * G / (2 * kPreRows)) + b + piece_row0 / (2 * kPreRows);
+  const int last = min(piece_row0 + 2 * kPreRows, n * G) - 1;  // the piece's last row
+  const int tiles = (sq.pos0 + last / G + kPreTile) / kPreTile, chunk = pre_chunk(tiles, args.splits);
+  if (chunk >= tiles) return;  // not cut
+  const int limit = sq.pos0 + ti + 1;
+  const int64_t row0 = (static_cast<int64_t>(slot) * a.c.Hkv + kvh) * args.splits * (2 * kPreRows) + row - piece_row0;
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int s = 0; s * chunk * kPreTile < limit; ++s) {  // parts of which the row sees something
+    const int64_t at = row0 + static_cast<int64_t>(s) * (2 * kPreRows);
+    const float2 ml = *reinterpret_cast<const float2*>(args.part_ml + 2 * at);
+    const float4 v = reinterpret_cast<const float4*>(args.part + at * kKv8D)[lane];
+    const float mn = fmaxf(m, ml.x);
+    const float f = m == -INFINITY ? 0.0f : ex2(m - mn), f2 = ml.x == -INFINITY ? 0.0f : ex2(ml.x - mn);
+    m = mn;
+    l = l * f + ml.y * f2;
+    o.x = o.x * f + v.x * f2;
+    o.y = o.y * f + v.y * f2;
+    o.z = o.z * f + v.z * f2;
+    o.w = o.w * f + v.w * f2;
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const __half2 y0 = __floats2half2_rn(o.x * inv, o.y * inv), y1 = __floats2half2_rn(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>(a.out + x * kKv8D + 4 * lane) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
 }
 
 }  // namespace w4a8

@@ -100,9 +100,10 @@ w4a8_status_t launch_kv8_decode(const CUtensorMap& map, const Kv8DecodeArgs& d, 
 // prefill kernel 2.3 us for 256 rows and 128 tokens, on one SM for each
 // (sequence, kv head): equal at 2700 / (B Hkv) rows while those are fewer than
 // the SMs, at 18 beyond. (Measured over 4000 cached tokens, 8 kv heads: 8
-// sequences of 64 rows 120 us in the one, 83 in the other; 1 of 256 rows 65
-// against 85.)
-int kv8_few_rows(int64_t B, int64_t Hkv) {
+// sequences of 64 rows 120 us in the one, 84 in the other; 1 of 256 rows 65
+// against 93.) A batch of 256 rows in all goes to the decode kernel whole.
+int kv8_few_rows(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
+  if (T * (Hq / Hkv) <= 256) return 256;
   const int64_t n = 2700 / (B * Hkv);
   return static_cast<int>(n < 18 ? 18 : n > 256 ? 256 : n);
 }
@@ -117,7 +118,7 @@ w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_c
   d.a = a;
   d.count = static_cast<int*>(workspace);
   d.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kDecMaxCtas * 4);
-  d.max_rows = a.s.q_start == nullptr ? G : kv8_few_rows(a.s.B, a.c.Hkv);
+  d.max_rows = a.s.q_start == nullptr ? G : kv8_few_rows(a.s.B, a.s.T, a.Hq, a.c.Hkv);
   // one CTA per SM, no more than the longest possible batch has tiles for
   const int64_t tiles = (c->max_blocks * c->page + kDecTile - 1) / kDecTile * a.s.B * a.c.Hkv *
                         ((d.max_rows + kDecCols - 1) / kDecCols);
@@ -127,21 +128,54 @@ w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_c
   return launch_kv8_decode<false>(map, d, static_cast<int>(grid), stream);
 }
 
-w4a8_status_t kv8_prefill(const Kv8AttnArgs& a, int few_rows, cudaStream_t stream) {
+// Pieces of 256 rows of the prefill kernel (sequence b's begin at slot start_b G
+// / 256 + b), and into how many parts each is cut: as many as fill the 148 SMs
+// where the pieces fill half of them at most.
+int64_t kv8_pre_slots(int64_t B, int64_t T, int64_t G) { return T * G / (2 * kPreRows) + B; }
+int kv8_pre_splits(int64_t slots, int64_t Hkv) {
+  const int64_t n = 148 / (slots * Hkv);
+  return static_cast<int>(n < 2 ? 1 : n > 32 ? 32 : n);
+}
+size_t kv8_pre_part_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
+  if (T * (Hq / Hkv) <= kv8_few_rows(B, T, Hq, Hkv)) return 0;
+  const int64_t slots = kv8_pre_slots(B, T, Hq / Hkv);
+  const int splits = kv8_pre_splits(slots, Hkv);
+  return splits > 1 ? static_cast<size_t>(slots * Hkv * splits) * (2 * kPreRows) * (kKv8D + 2) * 4 : 0;
+}
+constexpr size_t kDecWorkspace = kDecMaxCtas * (4 + 2 * kDecPart * sizeof(float));
+static_assert(kDecWorkspace % 256 == 0, "the prefill parts follow, aligned");
+
+template <bool CUT>
+w4a8_status_t launch_kv8_prefill(const Kv8PrefillArgs& p, cudaStream_t stream) {
   static bool done[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return launch_status();
   if (!done[dev]) {
-    if (cudaFuncSetAttribute(kv8_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PreSmem::kBytes) !=
+    if (cudaFuncSetAttribute(kv8_prefill_kernel<CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, PreSmem::kBytes) !=
         cudaSuccess)
       return launch_status();
     done[dev] = true;
   }
-  // slots of 256 rows: sequence b's begin at start_b G / 256 + b
-  const int64_t slots = static_cast<int64_t>(a.s.T) * (a.Hq / a.c.Hkv) / (2 * kPreRows) + a.s.B;
+  return launch_pdl(kv8_prefill_kernel<CUT>, dim3(static_cast<unsigned>(p.slots * p.a.c.Hkv * p.splits)),
+                    dim3(kPreThreads), PreSmem::kBytes, stream, 1, p);
+}
+
+w4a8_status_t kv8_prefill(const Kv8AttnArgs& a, int few_rows, void* workspace, cudaStream_t stream) {
+  const int64_t slots = kv8_pre_slots(a.s.B, a.s.T, a.Hq / a.c.Hkv);
   if (slots * a.c.Hkv > INT32_MAX) return W4A8_ERR_UNSUPPORTED_SHAPE;
-  return launch_pdl(kv8_prefill_kernel, dim3(static_cast<unsigned>(slots * a.c.Hkv)), dim3(kPreThreads),
-                    PreSmem::kBytes, stream, 1, a, static_cast<int>(slots), few_rows);
+  Kv8PrefillArgs p;
+  p.a = a;
+  p.slots = static_cast<int>(slots);
+  p.few_rows = few_rows;
+  p.splits = kv8_pre_splits(slots, a.c.Hkv);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kDecWorkspace);
+  p.part_ml = p.part + slots * a.c.Hkv * p.splits * (2 * kPreRows) * kKv8D;
+  if (p.splits == 1) return launch_kv8_prefill<false>(p, stream);
+  const w4a8_status_t st = launch_kv8_prefill<true>(p, stream);
+  if (st != W4A8_OK) return st;
+  const int64_t join = (static_cast<int64_t>(a.s.T) * a.Hq + kPreJoinWarps - 1) / kPreJoinWarps;
+  return launch_pdl(kv8_prefill_join_kernel, dim3(static_cast<unsigned>(join)), dim3(kPreJoinWarps * 32), 0, stream, 1,
+                    p);
 }
 
 w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int32_t* seq_lens, const int32_t* q_start,
@@ -170,11 +204,11 @@ w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int3
   // each kernel takes the sequences that suit it; one whose share must be
   // empty is not launched
   const int64_t rows = T * (Hq / c->Hkv);
-  const int few = kv8_few_rows(B, c->Hkv);
+  const int few = kv8_few_rows(B, T, Hq, c->Hkv);
   if (rows <= few) return kv8_decode(a, dev, c, workspace, stream);
-  if (B == 1) return kv8_prefill(a, 0, stream);
+  if (B == 1) return kv8_prefill(a, 0, workspace, stream);
   st = kv8_decode(a, dev, c, workspace, stream);
-  return st != W4A8_OK ? st : kv8_prefill(a, few, stream);
+  return st != W4A8_OK ? st : kv8_prefill(a, few, workspace, stream);
 }
 
 }  // namespace
@@ -245,8 +279,9 @@ w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cache_t* cach
 }
 
 size_t w4a8_kv8_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
-  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
-  return kDecMaxCtas * (4 + 2 * kDecPart * sizeof(float));
+  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || B > 65535 || T > INT32_MAX / 1024 || Hq > 1024)
+    return 0;
+  return kDecWorkspace + kv8_pre_part_bytes(B, T, Hq, Hkv);
 }
 
 w4a8_status_t w4a8_kv8_attention_decode(const void* q, const w4a8_kv8_cache_t* cache, const int32_t* seq_lens,
