@@ -95,17 +95,15 @@ w4a8_status_t launch_kv8_decode(const CUtensorMap& map, const Kv8DecodeArgs& d, 
 }
 
 // Sequences whose rows (new tokens times query heads per kv head) are at most
-// this many go to the decode kernel, others to the prefill kernel. The decode
-// kernel takes 0.25 us an SM for 8 rows and 32 tokens, spread over all SMs; the
-// prefill kernel 2.3 us for 256 rows and 128 tokens, on one SM for each
-// (sequence, kv head): equal at 2700 / (B Hkv) rows while those are fewer than
-// the SMs, at 18 beyond. (Measured over 4000 cached tokens, 8 kv heads: 8
-// sequences of 64 rows 120 us in the one, 84 in the other; 1 of 256 rows 65
-// against 93.) A batch of 256 rows in all goes to the decode kernel whole.
+// this many go to the decode kernel, which reads the cache once for 8 rows,
+// others to the prefill kernel, which reads it once for 256. Measured, 8 kv
+// heads (decode against prefill kernel): 1 sequence of 32 rows over 1000, 4000,
+// 32000 tokens 14, 24, 67 us against 23, 26, 55; of 64 rows 19, 29, 114 against
+// 24, 26, 56; 4 sequences of 32 rows over 1000, 4000 tokens 22, 43 against 25,
+// 37. Where several sequences have 160 rows in all, as many short guesses do,
+// all go to the decode kernel: the others' launches would do nothing for 5 us.
 int kv8_few_rows(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
-  if (T * (Hq / Hkv) <= 256) return 256;
-  const int64_t n = 2700 / (B * Hkv);
-  return static_cast<int>(n < 18 ? 18 : n > 256 ? 256 : n);
+  return B > 1 && T * (Hq / Hkv) <= 160 ? 160 : 32;
 }
 
 w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_cache_t* c, void* workspace,
