@@ -522,7 +522,8 @@ W4A8_API w4a8_status_t w4a8_rmsnorm_quantize_act(const void* X, const void* resi
  * output. A length above max_blocks * page or below the number of new tokens,
  * and a page outside [0, num_pages), are recorded as W4A8_DEVERR_KV_RANGE: the
  * append skips the tokens concerned, the attention gives values of that
- * sequence that mean nothing; no access leaves the buffers.
+ * sequence that mean nothing. A q_start that falls gives rows that mean nothing.
+ * No access leaves the buffers in any of these cases.
  */
 typedef struct {
   int8_t* codes;
@@ -544,7 +545,7 @@ typedef struct {
  * large position), its sine and cosine to 2^-20. inv_freq: fp32 [rotary_dim / 2] in device memory, as scaled
  * for long contexts by the caller; rope_scale: a factor on the rotated values
  * (1 for none).
- * q goes to q_out, fp16 [T, Hq, 128] (16-byte aligned); k and v (as fp32, not
+ * q goes to q_out, fp16 [T, Hq, 128] (16-byte aligned, no part of qkv); k and v (as fp32, not
  * rounded in between) into the cache. In every page that gets new tokens
  *   s' = max(s, fp32(max |new values| / 127)),  s = 0 if the page's first place is one of them
  *   codes that were there: rint(code * (s / s')) if s' > s
@@ -565,7 +566,7 @@ W4A8_API size_t w4a8_kv8_attention_workspace_bytes(int64_t B, int64_t T, int64_t
 
 /*
  * Attention of one new token per sequence over the cache that already holds
- * it. q, out: fp16 [B, Hq, 128] (16-byte aligned). Query head h reads kv head
+ * it. q, out: fp16 [B, Hq, 128] (16-byte aligned; out may be q). Query head h reads kv head
  * h / (Hq / Hkv);
  *   s_j = scale * sK * sum_d q[d] * codeK[j, d],  j < seq_lens[b]
  *   out[b, h] = fp16_rn(sum_j softmax(s)_j * sV * codeV[j])
@@ -583,7 +584,8 @@ W4A8_API w4a8_status_t w4a8_kv8_attention_decode(const void* q, const w4a8_kv8_c
 /*
  * The same for several new tokens per sequence (q_start as above, required),
  * causal: row i of sequence b's n_b rows sees its tokens j < seq_lens[b] - n_b
- * + i + 1. q, out: fp16 [T, Hq, 128]. workspace as for the decode call, of
+ * + i + 1. q, out: fp16 [T, Hq, 128] (out may be q). The softmax weights are
+ * rounded to fp16 for the product with the values, their sum is not. workspace as for the decode call, of
  * w4a8_kv8_attention_workspace_bytes(B, T, Hq, Hkv) bytes.
  */
 W4A8_API w4a8_status_t w4a8_kv8_attention_prefill(const void* q, const w4a8_kv8_cache_t* cache,

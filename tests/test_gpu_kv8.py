@@ -363,6 +363,77 @@ def test_attention_repeats_bit_for_bit_and_leaves_the_workspace_clean():
     assert int(bad) == 0
 
 
+def test_attention_output_in_place_of_the_query():
+    for c, decode in ((case(8, 2, 64, [1] * 3, [3000, 0, 700], 33), True), (case(8, 2, 64, [5, 300], [3000, 20], 34), False)):
+        ref = attend(c, decode)
+        g = [dev(a) for a in c]
+        if decode:
+            w4a8.kv8_attention_decode(*g[:5], SCALE, out=g[0])
+        else:
+            w4a8.kv8_attention_prefill(*g, SCALE, out=g[0])
+        assert np.array_equal(host(g[0]).view(np.uint16), ref.view(np.uint16))
+
+
+def test_attention_with_a_negative_and_a_zero_scale():
+    """Softmax of the negated scores; every token alike."""
+    for decode in (True, False):
+        c = case(8, 2, 32, [1, 1] if decode else [40, 3], [100, 20], 35)
+        g = [dev(a) for a in c]
+        call = (lambda s: w4a8.kv8_attention_decode(*g[:5], s)) if decode else (lambda s: w4a8.kv8_attention_prefill(*g, s))
+        y = host(call(-SCALE))
+        o, E = S.attention(*c, -SCALE, 2.0 ** -11, None, 2.0 ** -35)
+        ulp = np.spacing(np.maximum(np.abs(o) + E, 6.2e-5).astype(np.float16)).astype(np.float64)
+        assert (np.abs(y.astype(np.float64) - o) <= 0.5 * ulp + E).all()
+        y = host(call(0.0))
+        o, E = S.attention(*c, 0.0, 2.0 ** -11, None, 2.0 ** -35)
+        ulp = np.spacing(np.maximum(np.abs(o) + E, 6.2e-5).astype(np.float16)).astype(np.float64)
+        assert (np.abs(y.astype(np.float64) - o) <= 0.5 * ulp + E).all()
+
+
+def test_shared_pages_between_sequences():
+    """A common prefix held once: several tables name the same pages."""
+    for decode in (True, False):
+        c = list(case(8, 2, 32, [1, 1, 1] if decode else [30, 40, 2], [200, 230, 300], 36))
+        c[3] = c[3].copy()
+        c[3][1:, :6] = c[3][0, :6]
+        check_attention(c, attend(c, decode), 2.0 ** (-20 if decode else -11))
+
+
+def test_starts_that_fall_are_reported_and_stay_in_bounds():
+    c = list(case(4, 2, 16, [5, 9, 7], [20, 30, 40], 37))
+    c[5] = i32([0, 14, 5, 21])
+    g = [dev(a) for a in c]
+    w4a8.kv8_attention_prefill(*g, SCALE)
+    assert w4a8.get_device_error(DEV) == w4a8.DEVERR_KV_RANGE
+    w4a8.clear_device_error(DEV)
+    f, _ = w4a8.rope_frequencies(128, device=DEV)
+    qkv = torch.zeros((21, 8 * 128), dtype=torch.float16, device=DEV)
+    w4a8.kv8_rope_append(qkv, 4, g[1], g[2], g[3], g[4], f, q_start=dev(i32([-7, 14, 5, 1 << 30])))
+    assert w4a8.get_device_error(DEV) == w4a8.DEVERR_KV_RANGE
+    w4a8.clear_device_error(DEV)
+
+
+def test_prefill_in_a_graph_with_other_lengths():
+    c = case(8, 2, 64, [40, 300, 3], [3000, 20, 100], 38)
+    g = [dev(a) for a in c]
+    out = torch.empty_like(g[0])
+    w4a8.kv8_attention_prefill(*g, SCALE, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w4a8.kv8_attention_prefill(*g, SCALE, out=out)
+    new, old = [300, 3, 40], [20, 2900, 0]
+    start, lens = i32(np.concatenate([[0], np.cumsum(new)])), i32([n + o for n, o in zip(new, old)])
+    table = c[3].copy()
+    table[0], table[1] = c[3][1], c[3][0]
+    for t, a in zip(g[3:], (table, lens, start)):
+        t.copy_(dev(a))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    check_attention((c[0], c[1], c[2], table, lens, start), host(out), 2.0 ** -11, heads=(0, 5))
+
+
 def test_two_streams_at_once_without_a_workspace():
     """The binding keeps a workspace per stream: calls on two streams may overlap."""
     cs = [case(8, 2, 64, [1] * 3, [3000, 900, 2000], s) for s in (26, 27)]

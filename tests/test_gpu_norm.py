@@ -161,7 +161,8 @@ def test_norm_on_another_stream_and_in_a_graph():
 def test_norm_refuses_mismatched_tensors():
     x, w, r = (dev(a) for a in draw(4, 256, 51))
     bad = [dict(X=x.float()), dict(X=x[:, ::2]), dict(weight=w[:128]), dict(weight=w.float()), dict(residual=r[:2]),
-           dict(residual=r.cpu()), dict(out=(x, x, w, w))]
+           dict(residual=r.cpu()), dict(out=(x, x, w, w)),
+           dict(out=(None, x.to(torch.int8), x[:, 0].contiguous(), x[:, 0].int()))]
     for kw in bad:
         a = dict(X=x, weight=w, eps=EPS, residual=r)
         a.update(kw)

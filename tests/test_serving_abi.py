@@ -42,6 +42,7 @@ def desc(**kw):
 BAD_CACHES = [(dict(D=64), 2), (dict(page=48), 2), (dict(page=8), 2), (dict(Hkv=0), 2), (dict(Hkv=3), 2),
               (dict(Hkv=-1), 1), (dict(num_pages=0), 2), (dict(num_pages=-1), 1), (dict(max_blocks=0), 2),
               (dict(max_blocks=(1 << 24) // 64 + 1), 2), (dict(num_pages=1 << 24), 2), (dict(reserved=1), 1),
+              (dict(num_pages=1 << 62), 2), (dict(max_blocks=1 << 62), 2), (dict(num_pages=(1 << 31) // 256), 2),
               (dict(codes=None), 1), (dict(scales=None), 1), (dict(block_table=None), 1), (dict(codes=FAKE + 64), 3),
               (dict(scales=ODD), 3), (dict(block_table=ODD), 3)]
 

@@ -726,10 +726,12 @@ def rmsnorm_quantize_act(X, weight, eps, residual=None, out=None):
         H, r, h = None, None, None
     else:
         _check_tensor(residual, "residual", f16, dev, (M, K))
+        if H is None:
+            raise W4A8Error("out must hold H where there is a residual")
         _check_tensor(H, "H", f16, dev, (M, K))
         r, h = residual.data_ptr(), H.data_ptr()
-    _launch(dev, "w4a8_rmsnorm_quantize_act", lib().w4a8_rmsnorm_quantize_act, X.data_ptr(), r, weight.data_ptr(), eps,
-            M, K, h, A8.data_ptr(), sA.data_ptr(), rowsum.data_ptr())
+    _launch(dev, "w4a8_rmsnorm_quantize_act", lib().w4a8_rmsnorm_quantize_act, X.data_ptr(), r, weight.data_ptr(),
+            float(eps), M, K, h, A8.data_ptr(), sA.data_ptr(), rowsum.data_ptr())
     return H, A8, sA, rowsum
 
 
@@ -834,7 +836,8 @@ def kv8_rope_append(qkv, Hq: int, kv_codes, kv_scales, block_table, seq_lens, in
     else:
         _check_tensor(out, "out", f16, dev, (T, Hq, KV_HEAD_DIM))
     _launch(dev, "w4a8_kv8_rope_append", lib().w4a8_kv8_rope_append, qkv.data_ptr(), desc, seq_lens.data_ptr(), start,
-            B, T, Hq, inv_freq.data_ptr(), 2 * inv_freq.numel(), 1 if interleaved else 0, rope_scale, out.data_ptr())
+            B, T, Hq, inv_freq.data_ptr(), 2 * inv_freq.numel(), 1 if interleaved else 0, float(rope_scale),
+            out.data_ptr())
     return out
 
 
@@ -879,12 +882,12 @@ def _kv8_attention(what, q, kv_codes, kv_scales, block_table, seq_lens, scale, q
         _check_tensor(workspace, "workspace", torch.uint8, dev)
     L = lib()
     if q_start is None:
-        _launch(dev, what, L.w4a8_kv8_attention_decode, q.data_ptr(), desc, seq_lens.data_ptr(), B, Hq, scale,
+        _launch(dev, what, L.w4a8_kv8_attention_decode, q.data_ptr(), desc, seq_lens.data_ptr(), B, Hq, float(scale),
                 out.data_ptr(), workspace.data_ptr(), workspace.numel())
     else:
         _check_tensor(q_start, "q_start", torch.int32, dev, (B + 1,))
         _launch(dev, what, L.w4a8_kv8_attention_prefill, q.data_ptr(), desc, seq_lens.data_ptr(), q_start.data_ptr(),
-                B, T, Hq, scale, out.data_ptr(), workspace.data_ptr(), workspace.numel())
+                B, T, Hq, float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 

@@ -63,10 +63,12 @@ __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// As bulk waits elsewhere: bounded, and no return while copies are in flight.
-__device__ __forceinline__ void kv8_wait(uint64_t* bar, uint32_t parity, DevErr err) {
-  if (!mbar_wait_limit(bar, parity, nullptr, err, kErrKv8Wait, kWaitLimitNs))
-    mbar_wait_limit(bar, parity, nullptr, err, kErrKv8Wait, kWaitLimitNs);
+// A warp's bounded wait for copies; false (in every lane) if they are not there
+// after a second limit either.
+__device__ __forceinline__ bool kv8_wait(uint64_t* bar, uint32_t parity, DevErr err) {
+  const bool ok = mbar_wait_limit(bar, parity, nullptr, err, kErrKv8Wait, kWaitLimitNs) ||
+                  mbar_wait_limit(bar, parity, nullptr, err, kErrKv8Wait, kWaitLimitNs);
+  return __all_sync(0xffffffffu, ok) != 0;
 }
 
 // What bounds a decode step is reading the cache: 256 bytes per token and kv
@@ -154,6 +156,7 @@ __device__ __forceinline__ DecPair dec_sequence(const Kv8AttnArgs& a, int b, int
   const int64_t capacity = static_cast<int64_t>(a.c.max_blocks) * a.c.P;
   p.row0 = kv8_row_start(a.s, b);
   p.n = a.s.q_start == nullptr ? 1 : kv8_row_start(a.s, b + 1) - p.row0;
+  if (p.n < 0 && report) atomicCAS(a.err, 0, kErrKv8Range);
   if (p.n <= 0 || static_cast<int64_t>(p.n) * G > max_rows) return p;
   p.len = __ldg(a.s.seq_lens + b);
   const int least = a.s.q_start == nullptr ? 0 : p.n;
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(DecCfg<DUP>::kWarps * 32, 1)
     p.first = next;
   };
 
-  const int n_mine = static_cast<int>(we - ws);
+  int n_mine = static_cast<int>(we - ws);
   DecPair cur = locate(n_mine > 0 ? ws : cs), nxt = cur;  // consuming, requesting
   int64_t x_next = ws;
   int blk0 = 0, blk_b = -1;      // the window of the block table that the lanes hold
@@ -371,7 +374,15 @@ __global__ void __launch_bounds__(DecCfg<DUP>::kWarps * 32, 1)
     }
     const int tok0 = static_cast<int>(x - cur.first) * kDecTile;
     const int n = min(cur.len - tok0, kDecTile);
-    kv8_wait(bars + stage, phase, err);
+    if (!kv8_wait(bars + stage, phase, err)) {
+      // given up (reported): nothing more is requested, and the copies still
+      // under way get their limit before their memory is used for anything else
+      for (int i = 1; i < kStages && it + i < n_mine; ++i) {
+        const int s2 = (stage + i) % kStages;
+        kv8_wait(bars + s2, s2 > stage ? phase : phase ^ 1u, err);
+      }
+      n_mine = it + 1;
+    }
     if (n > 0) {
       const uint8_t* sk = ring + stage * kDecStageBytes;
       const uint8_t* sv = sk + kDecTile * kKv8D;

@@ -22,17 +22,18 @@ w4a8_status_t launch_rmsnorm(const __half* X, const __half* R, const __half* W, 
                     A8, sA, rowsum, early);
 }
 
-// Checks of a cache descriptor and of the batch's sizes. max_table: entries
-// the table is indexed with stay below 2^31 per sequence.
+// Checks of a cache descriptor and of the batch's sizes (each factor bounded
+// before the products are formed).
 w4a8_status_t check_kv8(const w4a8_kv8_cache_t* c, int64_t B, int64_t T, int64_t Hq) {
   if (c == nullptr) return W4A8_ERR_INVALID_ARG;
   if (c->reserved != 0 || B < 0 || T < 0 || Hq < 0 || c->num_pages < 0 || c->max_blocks < 0 || c->Hkv < 0)
     return W4A8_ERR_INVALID_ARG;
   if (c->D != kKv8D || !(c->page == 16 || c->page == 32 || c->page == 64 || c->page == 128))
     return W4A8_ERR_UNSUPPORTED_SHAPE;
-  if (c->Hkv == 0 || Hq == 0 || Hq % c->Hkv != 0 || Hq > 1024 || c->num_pages == 0 || c->max_blocks == 0 ||
-      c->max_blocks * c->page > kKv8MaxLen || c->num_pages * 2 * c->Hkv > INT32_MAX / c->page || B > 65535 ||
-      T > INT32_MAX / 1024)
+  if (c->Hkv == 0 || Hq == 0 || Hq > 1024 || Hq % c->Hkv != 0 || B > 65535 || T > INT32_MAX / 1024)
+    return W4A8_ERR_UNSUPPORTED_SHAPE;
+  if (c->num_pages == 0 || c->num_pages > INT32_MAX || c->num_pages * 2 * c->Hkv > INT32_MAX / c->page ||
+      c->max_blocks == 0 || c->max_blocks > kKv8MaxLen || c->max_blocks * c->page > kKv8MaxLen)
     return W4A8_ERR_UNSUPPORTED_SHAPE;
   return W4A8_OK;
 }
