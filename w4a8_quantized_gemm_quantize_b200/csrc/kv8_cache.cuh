@@ -84,7 +84,12 @@ struct Kv8AppendArgs {
   int* err;
 };
 
-constexpr int kKv8AppendThreads = 256;
+// Threads of an append block, by PAGE: the page's tokens, or 0 (below). Measured, 4 x 500 tokens, 32 + 2 x 8 heads: pages of 16 by 128
+// threads 11.9 us, by 256 16.7 (more of the blocks' short chains of dependent
+// reads run at once); of 32 by 128 11.7, by 256 14.1; of 64 by 128 16.4, by 256
+// 13.8, by 512 17.3 (by 128 a thread holds too much); of 128 by 512 18.1, by 256 19.3.
+__host__ __device__ constexpr int kv8_append_threads(int P) { return P <= 32 ? 128 : P == 64 ? 256 : 512; }
+__host__ __device__ constexpr int kv8_append_blocks(int P) { return P <= 32 ? 8 : P == 64 ? 4 : 2; }  // of an SM
 
 // The rotation of pair i at position pos: angle pos * f_i, taken in turns.
 // f_i / (2 pi) is held as a 64-bit fraction of a turn, so that the product
@@ -183,13 +188,19 @@ __device__ __forceinline__ void kv8_rotate(const Kv8Vec& r, const __half* vec, i
 // HBM-bound (2 bytes read per value, 2 or 1 written) for many rows; a decode
 // step is a chain of dependent reads (length, table, page scale). All of a
 // thread's reads are under way before the angles are worked out.
-template <int P, Kv8Layout L>
-__global__ void __launch_bounds__(kKv8AppendThreads, P <= 64 ? 4 : 2) kv8_append_kernel(Kv8AppendArgs a) {
-  constexpr int kSlab = kKv8AppendThreads / 16;  // tokens of the page a pass covers
-  constexpr int kPasses = P / kSlab;
+// PAGE: the page's tokens; 0: one new token per sequence in pages of 64 or 128,
+// where going through the whole page for it costs more. Measured, 64 such
+// sequences: pages of 64 4.4 us (through the page 6.1), of 128 4.3 (10.8); of 32
+// 4.4 (3.9), of 16 4.4 (3.6), which go through the page.
+template <int PAGE, Kv8Layout L>
+__global__ void __launch_bounds__(kv8_append_threads(PAGE), kv8_append_blocks(PAGE)) kv8_append_kernel(Kv8AppendArgs a) {
+  constexpr int kThreads = kv8_append_threads(PAGE);
+  const int P = PAGE > 0 ? PAGE : a.c.P;
+  constexpr int kSlab = kThreads / 16;  // tokens of the page a pass covers
+  constexpr int kPasses = PAGE > 0 ? PAGE / kSlab : 1;
   __shared__ uint64_t s_turns[kKv8D / 2];
   __shared__ __align__(16) float s_cos[2][kSlab][kKv8D / 2], s_sin[2][kSlab][kKv8D / 2];  // of a slab's tokens, two turns
-  __shared__ float s_red[kKv8AppendThreads / 32];
+  __shared__ float s_red[kThreads / 32];
   const int t = threadIdx.x;
   const int i = t & 15;  // lane of a vector
   const int half = a.rotary >> 1;
@@ -216,8 +227,8 @@ __global__ void __launch_bounds__(kKv8AppendThreads, P <= 64 ? 4 : 2) kv8_append
       if (row - q.first < q.n) pos[k] = q.pos0 + row - q.first;
     }
     __syncthreads();
-    {
-      const int k = t >> 6, f = t & 63;
+    for (int x = t; x < 256; x += kThreads) {
+      const int k = x >> 6, f = x & 63;
       const int p = k == 0 ? pos[0] : k == 1 ? pos[1] : k == 2 ? pos[2] : pos[3];
       if (f < half && p >= 0) kv8_cos_sin(s_turns[f], p, a.rope_scale, &s_cos[0][k][f], &s_sin[0][k][f]);
     }
@@ -227,16 +238,16 @@ __global__ void __launch_bounds__(kKv8AppendThreads, P <= 64 ? 4 : 2) kv8_append
       if (pos[k] < 0) continue;
       const __half* src = a.qkv + (row0 + k) * row_elems;
       __half* dst = a.q_out + static_cast<int64_t>(row0 + k) * a.Hq * kKv8D;
-      for (int v0 = t; v0 < a.Hq * 16; v0 += 2 * kKv8AppendThreads) {
+      for (int v0 = t; v0 < a.Hq * 16; v0 += 2 * kThreads) {
         Kv8Vec r[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int v = v0 + u * kKv8AppendThreads;
+          const int v = v0 + u * kThreads;
           if (v < a.Hq * 16) r[u] = kv8_load(src + (v >> 4) * kKv8D, lane);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int v = v0 + u * kKv8AppendThreads;
+          const int v = v0 + u * kThreads;
           if (v >= a.Hq * 16) break;
           float o[8];
           kv8_rotate<L>(r[u], src + (v >> 4) * kKv8D, i, s_cos[0][k], s_sin[0][k], a.rotary, o);
@@ -268,8 +279,9 @@ __global__ void __launch_bounds__(kKv8AppendThreads, P <= 64 ? 4 : 2) kv8_append
   }
   const Kv8Seq q = kv8_sequence(a.s, b, capacity, t == 0 ? a.err : nullptr);
   if (q.n <= 0) return;
-  const int page_no = q.pos0 / P + k;
-  if (page_no > (q.len - 1) / P) return;
+  const int shift = PAGE > 0 ? 0 : __ffs(P) - 1;  // (a division by a page not known here costs 0.4 us)
+  const int page_no = (PAGE > 0 ? q.pos0 / P : q.pos0 >> shift) + k;
+  if (page_no > (PAGE > 0 ? (q.len - 1) / P : (q.len - 1) >> shift)) return;
   const int base = page_no * P;                                     // position of the page's first place
   const int lo = max(q.pos0 - base, 0), hi = min(q.len - base, P);  // places [lo, hi) are new
   const bool is_k = kh < a.c.Hkv;
@@ -277,10 +289,11 @@ __global__ void __launch_bounds__(kKv8AppendThreads, P <= 64 ? 4 : 2) kv8_append
   const __half* src = a.qkv + (static_cast<int64_t>(q.first) + base - q.pos0) * row_elems +
                       static_cast<int64_t>(a.Hq + kh) * kKv8D;  // place 0 of the page (read from place lo on)
   const Kv8Lane lane = kv8_lane<L>(i, rotary);
+  const int slab0 = PAGE > 0 ? 0 : lo & ~(kSlab - 1);  // where the passes begin
   Kv8Vec raw[kPasses];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int j = p * kSlab + (t >> 4);
+    const int j = slab0 + p * kSlab + (t >> 4);
     if (j >= lo && j < hi) raw[p] = kv8_load(src + j * row_elems, lane);
   }
   const int page = __ldg(a.c.table + static_cast<int64_t>(b) * a.c.max_blocks + page_no);
@@ -296,8 +309,8 @@ __global__ void __launch_bounds__(kKv8AppendThreads, P <= 64 ? 4 : 2) kv8_append
   if (is_k) __syncthreads();  // s_turns
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int j = p * kSlab + (t >> 4);
-    const bool some = (p + 1) * kSlab > lo && p * kSlab < hi;  // the slab holds new tokens
+    const int j = slab0 + p * kSlab + (t >> 4);
+    const bool some = slab0 + (p + 1) * kSlab > lo && slab0 + p * kSlab < hi;  // the slab holds new tokens
     if (is_k && some) {
       for (int f = i; f < half; f += 16)
         kv8_cos_sin(s_turns[f], base + j, a.rope_scale, &s_cos[p & 1][t >> 4][f], &s_sin[p & 1][t >> 4][f]);
@@ -314,12 +327,12 @@ __global__ void __launch_bounds__(kKv8AppendThreads, P <= 64 ? 4 : 2) kv8_append
   if ((t & 31) == 0) s_red[t >> 5] = amax;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kKv8AppendThreads / 32; ++w) amax = fmaxf(amax, s_red[w]);
+  for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_red[w]);
   const float s_new = fmaxf(s_old, __fdiv_rn(amax, 127.0f));
   const float r = s_new > 0.0f ? __fdiv_rn(1.0f, s_new) : 0.0f;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int j = p * kSlab + (t >> 4);
+    const int j = slab0 + p * kSlab + (t >> 4);
     if (j >= lo && j < hi) {
       uint32_t w[2] = {0u, 0u};
 #pragma unroll
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(kKv8AppendThreads, P <= 64 ? 4 : 2) kv8_append
   }
   if (lo > 0 && s_new > s_old) {  // the codes that were there, carried over to the larger scale
     const float ratio = __fdiv_rn(s_old, s_new);
-    for (int v = t; v < lo * 16; v += kKv8AppendThreads) {
+    for (int v = t; v < lo * 16; v += kThreads) {
       uint2* at = reinterpret_cast<uint2*>(codes) + v;
       const uint2 c = *at;
       uint32_t w[2] = {c.x, c.y}, u[2] = {0u, 0u};

@@ -54,8 +54,9 @@ Kv8Cache kv8_cache_args(const w4a8_kv8_cache_t* c) {
 
 template <Kv8Layout L>
 w4a8_status_t launch_kv8_append(int page, dim3 grid, cudaStream_t st, const Kv8AppendArgs& a) {
-  const dim3 block(kKv8AppendThreads);
+  const dim3 block(static_cast<unsigned>(kv8_append_threads(page)));
   switch (page) {
+    case 0: return launch_pdl(kv8_append_kernel<0, L>, grid, block, 0, st, 1, a);
     case 16: return launch_pdl(kv8_append_kernel<16, L>, grid, block, 0, st, 1, a);
     case 32: return launch_pdl(kv8_append_kernel<32, L>, grid, block, 0, st, 1, a);
     case 64: return launch_pdl(kv8_append_kernel<64, L>, grid, block, 0, st, 1, a);
@@ -272,9 +273,10 @@ w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cache_t* cach
   if (grid > INT32_MAX) return W4A8_ERR_UNSUPPORTED_SHAPE;
   const dim3 g(static_cast<unsigned>(grid));
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (interleaved) return launch_kv8_append<kPairs>(cache->page, g, cs, a);
-  if (rotary_dim % 8 == 0) return launch_kv8_append<kSplit>(cache->page, g, cs, a);
-  return launch_kv8_append<kSingle>(cache->page, g, cs, a);
+  const int page = q_start == nullptr && cache->page > 32 ? 0 : cache->page;
+  if (interleaved) return launch_kv8_append<kPairs>(page, g, cs, a);
+  if (rotary_dim % 8 == 0) return launch_kv8_append<kSplit>(page, g, cs, a);
+  return launch_kv8_append<kSingle>(page, g, cs, a);
 }
 
 size_t w4a8_kv8_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
