@@ -13,6 +13,7 @@
 // carried over, c' = rint(c * (s / s')). A page whose first place is written
 // by the call starts from s = 0, whatever its last owner left there.
 #pragma once
+#include "codes.cuh"
 #include "ptx.cuh"
 
 namespace w4a8 {
@@ -84,10 +85,11 @@ struct Kv8AppendArgs {
   int* err;
 };
 
-// Threads of an append block, by PAGE: the page's tokens, or 0 (below). Measured, 4 x 500 tokens, 32 + 2 x 8 heads: pages of 16 by 128
-// threads 11.9 us, by 256 16.7 (more of the blocks' short chains of dependent
-// reads run at once); of 32 by 128 11.7, by 256 14.1; of 64 by 128 16.4, by 256
-// 13.8, by 512 17.3 (by 128 a thread holds too much); of 128 by 512 18.1, by 256 19.3.
+// Threads of an append block, by PAGE: the page's tokens, or 0 (below). Measured,
+// 4 x 500 tokens, 32 + 2 x 8 heads: pages of 16 by 128 threads 10.7 us, by 256
+// 14.9 (more of the blocks' short chains of dependent reads run at once); of 32
+// by 128 9.5, by 256 12.1; of 64 by 256 11.2, by 128 12.1 (a thread holds too
+// much); of 128 by 512 13.6, by 256 14.1.
 __host__ __device__ constexpr int kv8_append_threads(int P) { return P <= 32 ? 128 : P == 64 ? 256 : 512; }
 __host__ __device__ constexpr int kv8_append_blocks(int P) { return P <= 32 ? 8 : P == 64 ? 4 : 2; }  // of an SM
 
@@ -143,12 +145,35 @@ __device__ __forceinline__ void kv8_to_float(const uint2& v, float* o) {
   o[2] = b.x;
   o[3] = b.y;
 }
+// Where a lane has the cosines and sines of its pairs from.
+struct Kv8Table {  // a row's, in shared memory
+  const float* c;
+  const float* s;
+  __device__ __forceinline__ void four(int i, float (&ca)[4], float (&sa)[4]) const {
+    const float4 cv = *reinterpret_cast<const float4*>(c + 4 * i), sv = *reinterpret_cast<const float4*>(s + 4 * i);
+    ca[0] = cv.x, ca[1] = cv.y, ca[2] = cv.z, ca[3] = cv.w;
+    sa[0] = sv.x, sa[1] = sv.y, sa[2] = sv.z, sa[3] = sv.w;
+  }
+  __device__ __forceinline__ void one(int j, float* cj, float* sj) const {
+    *cj = c[j];
+    *sj = s[j];
+  }
+};
+struct Kv8Direct {  // worked out
+  const uint64_t* turns;
+  int pos;
+  float scale;
+  __device__ __forceinline__ void four(int i, float (&ca)[4], float (&sa)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) kv8_cos_sin(turns[4 * i + e], pos, scale, &ca[e], &sa[e]);
+  }
+  __device__ __forceinline__ void one(int j, float* cj, float* sj) const { kv8_cos_sin(turns[j], pos, scale, cj, sj); }
+};
 // The lane's values (o[0..3] from lo, o[4..7] from hi), rotated: (a, b) -> (a
-// cos - b sin, a sin + b cos). c, s: this token's cosine and sine of each pair;
-// vec: the vector (kSingle).
-template <Kv8Layout L>
-__device__ __forceinline__ void kv8_rotate(const Kv8Vec& r, const __half* vec, int i, const float* c, const float* s,
-                                           int rotary, float (&o)[8]) {
+// cos - b sin, a sin + b cos). vec: the vector (kSingle).
+template <Kv8Layout L, typename Angles>
+__device__ __forceinline__ void kv8_rotate(const Kv8Vec& r, const __half* vec, int i, const Angles& angles, int rotary,
+                                           float (&o)[8]) {
   kv8_to_float(r.lo, o);
   kv8_to_float(r.hi, o + 4);
   const int half = rotary >> 1;
@@ -159,23 +184,95 @@ __device__ __forceinline__ void kv8_rotate(const Kv8Vec& r, const __half* vec, i
       if (d < rotary) {
         const int j = d < half ? d : d - half;
         const float y = __half2float(vec[d < half ? d + half : j]);
-        o[e] = d < half ? o[e] * c[j] - y * s[j] : y * s[j] + o[e] * c[j];
+        float c, s;
+        angles.one(j, &c, &s);
+        o[e] = d < half ? o[e] * c - y * s : y * s + o[e] * c;
       }
     }
   } else if (4 * i < half) {
     // (kPairs: a rotary that 8 does not divide ends inside a lane's pairs)
-    const float4 cv = *reinterpret_cast<const float4*>(c + 4 * i), sv = *reinterpret_cast<const float4*>(s + 4 * i);
-    const float ca[4] = {cv.x, cv.y, cv.z, cv.w}, sa[4] = {sv.x, sv.y, sv.z, sv.w};
+    float c[4], s[4];
+    angles.four(i, c, s);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float& x = o[L == kSplit ? e : 2 * e];
       float& y = o[L == kSplit ? e + 4 : 2 * e + 1];
-      const float u = x * ca[e] - y * sa[e], v = x * sa[e] + y * ca[e];
+      const float u = x * c[e] - y * s[e], v = x * s[e] + y * c[e];
       if (L == kSplit || 4 * i + e < half) {
         x = u;
         y = v;
       }
     }
+  }
+}
+
+// R rows of q, every head of them, so that the angles are worked out once a row.
+// A thread's first reads are under way before the rows' positions are known.
+template <int R, Kv8Layout L, int THREADS>
+__device__ __forceinline__ void kv8_rotate_q(const Kv8AppendArgs& a, int64_t capacity, const uint64_t* s_turns,
+                                             float (*s_cos)[kKv8D / 2], float (*s_sin)[kKv8D / 2]) {
+  constexpr int kDepth = R == 1 ? 2 : 1;  // a row's vectors that a thread has under way at once
+  const int t = threadIdx.x;
+  const int i = t & 15;
+  const int half = a.rotary >> 1;
+  const int row0 = static_cast<int>(blockIdx.x) * R;
+  const int rows = min(R, a.s.T - row0);
+  const int vectors = a.Hq * 16;
+  const int64_t row_elems = static_cast<int64_t>(a.Hq + 2 * a.c.Hkv) * kKv8D;
+  const __half* src = a.qkv + row0 * row_elems;
+  __half* dst = a.q_out + static_cast<int64_t>(row0) * vectors * 8;
+  const Kv8Lane lane = kv8_lane<L>(i, a.rotary);
+  Kv8Vec r[R][kDepth];
+  const auto load = [&](int v0) {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int u = 0; u < kDepth; ++u) {
+        const int v = v0 + u * THREADS;
+        if (k < rows && v < vectors) r[k][u] = kv8_load(src + k * row_elems + (v >> 4) * kKv8D, lane);
+      }
+  };
+  load(t);
+  // every row's position, -1 for one that is left as it is
+  int pos[R];
+  Kv8Seq q = {0, -1, 0, 0};
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    pos[k] = -1;
+    const int row = row0 + k;
+    if (k >= rows) continue;
+    if (k == 0 || row - q.first >= q.n) {
+      const int b = a.s.q_start == nullptr ? row : kv8_find(a.s, row, 1, 1, 0);
+      if (b < 0) continue;
+      q = kv8_sequence(a.s, b, capacity, t == 0 ? a.err : nullptr);
+    }
+    if (row - q.first < q.n) pos[k] = q.pos0 + row - q.first;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+    if (THREADS >= R * 64 ? (t >> 6) == k : (t >> 6) == k % (THREADS / 64))
+      if ((t & 63) < half && pos[k] >= 0)
+        kv8_cos_sin(s_turns[t & 63], pos[k], a.rope_scale, &s_cos[k][t & 63], &s_sin[k][t & 63]);
+  __syncthreads();
+  for (int v0 = t; v0 < vectors; v0 += kDepth * THREADS) {
+    if (v0 != t) load(v0);
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int u = 0; u < kDepth; ++u) {
+        const int v = v0 + u * THREADS;
+        if (pos[k] < 0 || v >= vectors) continue;
+        float o[8];
+        kv8_rotate<L>(r[k][u], src + k * row_elems + (v >> 4) * kKv8D, i, Kv8Table{s_cos[k], s_sin[k]}, a.rotary, o);
+        uint2 w[2];
+        __half2* h = reinterpret_cast<__half2*>(w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(o[2 * j], o[2 * j + 1]);
+        __half* to = dst + (k * a.Hq + (v >> 4)) * kKv8D;
+        *reinterpret_cast<uint2*>(to + lane.lo) = w[0];
+        *reinterpret_cast<uint2*>(to + lane.hi) = w[1];
+      }
   }
 }
 
@@ -185,21 +282,25 @@ __device__ __forceinline__ void kv8_rotate(const Kv8Vec& r, const __half* vec, i
 // the read to the codes, so that the maximum over the page comes before the
 // first code.
 //
-// HBM-bound (2 bytes read per value, 2 or 1 written) for many rows; a decode
-// step is a chain of dependent reads (length, table, page scale). All of a
-// thread's reads are under way before the angles are worked out.
-// PAGE: the page's tokens; 0: one new token per sequence in pages of 64 or 128,
-// where going through the whole page for it costs more. Measured, 64 such
-// sequences: pages of 64 4.4 us (through the page 6.1), of 128 4.3 (10.8); of 32
-// 4.4 (3.9), of 16 4.4 (3.6), which go through the page.
+// HBM-bound (2 bytes read per value, 2 or 1 written) for many rows: 8200 tokens,
+// 32 + 2 x 8 heads, 184 MB, 37 us (5.0 TB/s); the rows of q alone run at 5.5
+// TB/s, the pages are held up by the chain of reads in front of theirs (length,
+// start, page). A decode step is that chain: 16 sequences 2.2 us. All of a thread's
+// reads are under way before the angles are worked out, and a page's angles by
+// the thread that rotates with them: sharing them among a block's threads
+// through shared memory took a barrier a slab and 42 us.
+//
+// PAGE: the page's tokens; 0: one new token per sequence in pages of any size,
+// by the one slab that holds it. Measured, 64 such sequences, pages of 16 / 32 /
+// 64 / 128: 3.1 us each; through the whole page 3.3 / 3.7 / 5.3 / 9.3.
 template <int PAGE, Kv8Layout L>
 __global__ void __launch_bounds__(kv8_append_threads(PAGE), kv8_append_blocks(PAGE)) kv8_append_kernel(Kv8AppendArgs a) {
   constexpr int kThreads = kv8_append_threads(PAGE);
   const int P = PAGE > 0 ? PAGE : a.c.P;
   constexpr int kSlab = kThreads / 16;  // tokens of the page a pass covers
   constexpr int kPasses = PAGE > 0 ? PAGE / kSlab : 1;
-  __shared__ uint64_t s_turns[kKv8D / 2];
-  __shared__ __align__(16) float s_cos[2][kSlab][kKv8D / 2], s_sin[2][kSlab][kKv8D / 2];  // of a slab's tokens, two turns
+  __shared__ __align__(16) uint64_t s_turns[kKv8D / 2];
+  __shared__ __align__(16) float s_cos[4][kKv8D / 2], s_sin[4][kKv8D / 2];  // of the rows of q
   __shared__ float s_red[kThreads / 32];
   const int t = threadIdx.x;
   const int i = t & 15;  // lane of a vector
@@ -210,56 +311,10 @@ __global__ void __launch_bounds__(kv8_append_threads(PAGE), kv8_append_blocks(PA
   const int64_t capacity = static_cast<int64_t>(a.c.max_blocks) * P;
   const int64_t row_elems = static_cast<int64_t>(a.Hq + 2 * a.c.Hkv) * kKv8D;
   if (static_cast<int>(blockIdx.x) < a.q_blocks) {
-    const int row0 = static_cast<int>(blockIdx.x) * a.q_rows;
-    const Kv8Lane lane = kv8_lane<L>(i, a.rotary);
-    // every row's position, -1 for one that is left as it is
-    int pos[4] = {-1, -1, -1, -1};
-    Kv8Seq q = {0, -1, 0, 0};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int row = row0 + k;
-      if (k >= a.q_rows || row >= a.s.T) break;
-      if (k == 0 || row - q.first >= q.n) {
-        const int b = a.s.q_start == nullptr ? row : kv8_find(a.s, row, 1, 1, 0);
-        if (b < 0) continue;
-        q = kv8_sequence(a.s, b, capacity, t == 0 ? a.err : nullptr);
-      }
-      if (row - q.first < q.n) pos[k] = q.pos0 + row - q.first;
-    }
-    __syncthreads();
-    for (int x = t; x < 256; x += kThreads) {
-      const int k = x >> 6, f = x & 63;
-      const int p = k == 0 ? pos[0] : k == 1 ? pos[1] : k == 2 ? pos[2] : pos[3];
-      if (f < half && p >= 0) kv8_cos_sin(s_turns[f], p, a.rope_scale, &s_cos[0][k][f], &s_sin[0][k][f]);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (pos[k] < 0) continue;
-      const __half* src = a.qkv + (row0 + k) * row_elems;
-      __half* dst = a.q_out + static_cast<int64_t>(row0 + k) * a.Hq * kKv8D;
-      for (int v0 = t; v0 < a.Hq * 16; v0 += 2 * kThreads) {
-        Kv8Vec r[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int v = v0 + u * kThreads;
-          if (v < a.Hq * 16) r[u] = kv8_load(src + (v >> 4) * kKv8D, lane);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int v = v0 + u * kThreads;
-          if (v >= a.Hq * 16) break;
-          float o[8];
-          kv8_rotate<L>(r[u], src + (v >> 4) * kKv8D, i, s_cos[0][k], s_sin[0][k], a.rotary, o);
-          uint2 w[2];
-          __half2* h = reinterpret_cast<__half2*>(w);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(o[2 * j], o[2 * j + 1]);
-          *reinterpret_cast<uint2*>(dst + (v >> 4) * kKv8D + lane.lo) = w[0];
-          *reinterpret_cast<uint2*>(dst + (v >> 4) * kKv8D + lane.hi) = w[1];
-        }
-      }
-    }
+    if (a.q_rows == 1)
+      kv8_rotate_q<1, L, kThreads>(a, capacity, s_turns, s_cos, s_sin);
+    else
+      kv8_rotate_q<4, L, kThreads>(a, capacity, s_turns, s_cos, s_sin);
     return;
   }
   // item: a page that the call writes to. Sequence b's pages start at item
@@ -279,7 +334,7 @@ __global__ void __launch_bounds__(kv8_append_threads(PAGE), kv8_append_blocks(PA
   }
   const Kv8Seq q = kv8_sequence(a.s, b, capacity, t == 0 ? a.err : nullptr);
   if (q.n <= 0) return;
-  const int shift = PAGE > 0 ? 0 : __ffs(P) - 1;  // (a division by a page not known here costs 0.4 us)
+  const int shift = PAGE > 0 ? 0 : __ffs(P) - 1;  // (a division by it costs 0.4 us)
   const int page_no = (PAGE > 0 ? q.pos0 / P : q.pos0 >> shift) + k;
   if (page_no > (PAGE > 0 ? (q.len - 1) / P : (q.len - 1) >> shift)) return;
   const int base = page_no * P;                                     // position of the page's first place
@@ -310,14 +365,8 @@ __global__ void __launch_bounds__(kv8_append_threads(PAGE), kv8_append_blocks(PA
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int j = slab0 + p * kSlab + (t >> 4);
-    const bool some = slab0 + (p + 1) * kSlab > lo && slab0 + p * kSlab < hi;  // the slab holds new tokens
-    if (is_k && some) {
-      for (int f = i; f < half; f += 16)
-        kv8_cos_sin(s_turns[f], base + j, a.rope_scale, &s_cos[p & 1][t >> 4][f], &s_sin[p & 1][t >> 4][f]);
-      __syncthreads();  // (a slab's angles are overwritten two slabs, one barrier, later)
-    }
     if (j >= lo && j < hi) {
-      kv8_rotate<L>(raw[p], src + j * row_elems, i, s_cos[p & 1][t >> 4], s_sin[p & 1][t >> 4], rotary, x[p]);
+      kv8_rotate<L>(raw[p], src + j * row_elems, i, Kv8Direct{s_turns, base + j, a.rope_scale}, rotary, x[p]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[p][e]));
     }
@@ -329,19 +378,14 @@ __global__ void __launch_bounds__(kv8_append_threads(PAGE), kv8_append_blocks(PA
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_red[w]);
   const float s_new = fmaxf(s_old, __fdiv_rn(amax, 127.0f));
-  const float r = s_new > 0.0f ? __fdiv_rn(1.0f, s_new) : 0.0f;
+  const float r = s_new > 1e-37f ? __fdiv_rn(1.0f, s_new) : 0.0f;  // (below it the reciprocal may not be finite)
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int j = slab0 + p * kSlab + (t >> 4);
     if (j >= lo && j < hi) {
-      uint32_t w[2] = {0u, 0u};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = max(-127, min(127, __float2int_rn(x[p][e] * r)));
-        w[e >> 2] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (e & 3));
-      }
-      *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.lo) = w[0];
-      *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.hi) = w[1];
+      // (|x| r <= 127 (1 + 2^-22): no code is beyond 127)
+      *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.lo) = pack_codes(x[p], r);
+      *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.hi) = pack_codes(x[p] + 4, r);
     }
   }
   if (lo > 0 && s_new > s_old) {  // the codes that were there, carried over to the larger scale

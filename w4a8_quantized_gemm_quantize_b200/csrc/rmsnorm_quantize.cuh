@@ -14,6 +14,7 @@
 // HBM-bound (2 + 2 bytes read, 2 + 1 written per element). One CTA per row,
 // the row in registers from the first read to the codes.
 #pragma once
+#include "codes.cuh"
 #include "quantize_act.cuh"
 
 namespace w4a8 {
@@ -34,16 +35,6 @@ __device__ __forceinline__ float block_all(float v, float* red) {
 #pragma unroll
   for (int i = 1; i < THREADS / 32; ++i) v = MAX ? fmaxf(v, red[i]) : v + red[i];
   return v;
-}
-
-// Codes of four values in units of the scale, |v * inv| < 2^21: rint of the
-// exact product (ties to even) by one fused multiply-add into the unit range of
-// 1.5 * 2^23, whose low byte is then the code.
-__device__ __forceinline__ uint32_t pack_codes(const float* v, float inv) {
-  constexpr float kMagic = 12582912.0f;
-  const uint32_t c0 = __float_as_uint(fmaf(v[0], inv, kMagic)), c1 = __float_as_uint(fmaf(v[1], inv, kMagic));
-  const uint32_t c2 = __float_as_uint(fmaf(v[2], inv, kMagic)), c3 = __float_as_uint(fmaf(v[3], inv, kMagic));
-  return __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
 }
 
 // VPT: 16-byte vectors (8 halves) per thread; K <= THREADS * VPT * 8. KEEP: the

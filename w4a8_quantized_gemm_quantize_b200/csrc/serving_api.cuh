@@ -273,7 +273,7 @@ w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cache_t* cach
   if (grid > INT32_MAX) return W4A8_ERR_UNSUPPORTED_SHAPE;
   const dim3 g(static_cast<unsigned>(grid));
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  const int page = q_start == nullptr && cache->page > 32 ? 0 : cache->page;
+  const int page = q_start == nullptr ? 0 : cache->page;
   if (interleaved) return launch_kv8_append<kPairs>(page, g, cs, a);
   if (rotary_dim % 8 == 0) return launch_kv8_append<kSplit>(page, g, cs, a);
   return launch_kv8_append<kSingle>(page, g, cs, a);
