@@ -549,7 +549,7 @@ typedef struct {
  * rounded in between) into the cache. In every page that gets new tokens
  *   s' = max(s, fp32(max |new values| / 127)),  s = 0 if the page's first place is one of them
  *   codes that were there: rint(code * (s / s')) if s' > s
- *   new codes: clamp(rint(x * (1 / s')), -127, 127)   (ties to even; s' == 0 gives zeros)
+ *   new codes: clamp(rint(x / s'), -127, 127)   (ties to even; s' < 1e-37 gives zeros)
  * and s' becomes its scale. Places behind the new tokens are left as they are.
  * A page that gets new tokens must not be shared with another sequence of the
  * batch. Non-finite inputs are a precondition violation (that page's contents

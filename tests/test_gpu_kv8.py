@@ -162,6 +162,30 @@ def test_append_of_zeros_and_a_stale_page():
     assert torch.equal(scales[1, 1], torch.full((1,), 2.0, device=DEV) / 127)
 
 
+@pytest.mark.parametrize("P", [16, 64])
+def test_append_codes_midway_go_to_the_even_one(P):
+    """Values and keys (without rotation: position 0) of a page whose scale is 6 or 14 exactly: x / s is exact
+    in 64 bits, many of them midway between two codes."""
+    n = P
+    v = np.arange(n * 128).reshape(n, 128)
+    x = np.zeros((n, 3, 128))
+    x[0, 1] = 7 * (v[0] % 255 - 127)   # K, position 0: |x| <= 889, multiples of 7 = s / 2
+    x[0, 1, 0] = 14 * 127
+    x[:, 2] = 3 * (v % 255 - 127)      # V: multiples of 3 = s / 2, |x| <= 381
+    x[0, 2, 0] = 6 * 127
+    codes, scales = w4a8.kv8_cache(1, 1, P, DEV)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    f = dev(np.ones(64, np.float32))
+    one = torch.ones(1, dtype=torch.int32, device=DEV)
+    # the keys' page holds the first token alone, so that no other key sets its scale
+    w4a8.kv8_rope_append(dev(x[:1].astype(np.float16)).reshape(1, -1), 1, codes, scales, table, one, f)
+    assert scales[0, 0, 0] == 14 and (codes[0, 0, 0, 0].cpu().numpy() == np.rint(x[0, 1] / 14)).all()
+    assert scales[0, 1, 0] == 6 and (codes[0, 1, 0, 0].cpu().numpy() == np.rint(x[0, 2] / 6)).all()
+    start = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    w4a8.kv8_rope_append(dev(x.astype(np.float16)).reshape(n, -1), 1, codes, scales, table, one * n, f, q_start=start)
+    assert scales[0, 1, 0] == 6 and (codes[0, 1, 0].cpu().numpy() == np.rint(x[:, 2] / 6)).all()
+
+
 def test_append_reports_what_it_cannot_place():
     """Lengths beyond the table, pages outside the pool: skipped and reported; the others are placed."""
     codes, scales = w4a8.kv8_cache(4, 1, 16, DEV)

@@ -89,7 +89,7 @@ struct Kv8AppendArgs {
 // 4 x 500 tokens, 32 + 2 x 8 heads: pages of 16 by 128 threads 10.7 us, by 256
 // 14.9 (more of the blocks' short chains of dependent reads run at once); of 32
 // by 128 9.5, by 256 12.1; of 64 by 256 11.2, by 128 12.1 (a thread holds too
-// much); of 128 by 512 13.6, by 256 14.1.
+// much); of 128 by 512 13.6, by 256 14.1 (all with the cheaper angles below).
 __host__ __device__ constexpr int kv8_append_threads(int P) { return P <= 32 ? 128 : P == 64 ? 256 : 512; }
 __host__ __device__ constexpr int kv8_append_blocks(int P) { return P <= 32 ? 8 : P == 64 ? 4 : 2; }  // of an SM
 
@@ -97,18 +97,27 @@ __host__ __device__ constexpr int kv8_append_blocks(int P) { return P <= 32 ? 8 
 // f_i / (2 pi) is held as a 64-bit fraction of a turn, so that the product
 // with the position wraps at whole turns by itself and is exact to 2^-29 of a
 // turn at position 2^24 (an fp32 product is off by 2^-24 * pos * f radians,
-// 0.008 at position 131072). Its top 32 bits give the angle in [-pi, pi), where
-// the hardware's sine and cosine are within 2^-20.5: far below a half step of
-// the fp16 (2^-11) or 8-bit (2^-8) values that come of it.
+// 0.008 at position 131072). Its top 32 bits give the quarter turn and the
+// angle within it, in [-pi / 4, pi / 4], where the Taylor series' next terms are
+// below 2^-25. The sine and cosine come out within 2^-23, so that an
+// angle moves a code by 127 * 2^-23 of a step and few lie that near the middle
+// between two. (The hardware's approximations, within 2^-20.5, took 37.1 us
+// where these take 39.6: six times as many codes go to the farther of two.)
 __device__ __forceinline__ uint64_t kv8_turns(float f) {
   const double t = static_cast<double>(f) * 0.15915494309189533577;  // 1 / (2 pi)
   return static_cast<uint64_t>((t - floor(t)) * 18446744073709551616.0);
 }
 __device__ __forceinline__ void kv8_cos_sin(uint64_t turns, int pos, float scale, float* c, float* s) {
-  const int32_t top = static_cast<int32_t>((turns * static_cast<uint64_t>(pos)) >> 32);
-  const float angle = static_cast<float>(top) * 1.4629180792671596e-9f;  // pi / 2^31
-  *c = __cosf(angle) * scale;
-  *s = __sinf(angle) * scale;
+  const uint32_t top = static_cast<uint32_t>((turns * static_cast<uint64_t>(pos)) >> 32);
+  const uint32_t quarter = (top + 0x20000000u) >> 30;
+  const float a = static_cast<float>(static_cast<int32_t>(top - (quarter << 30))) * 1.4629180792671596e-9f;  // pi / 2^31
+  const float a2 = a * a;
+  const float sa = fmaf(a * a2, fmaf(a2, fmaf(a2, fmaf(a2, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), a);
+  const float ca = fmaf(a2, fmaf(a2, fmaf(a2, fmaf(a2, 1.0f / 40320, -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+  const bool odd = (quarter & 1u) != 0;
+  // (the quarter's signs as the sign bits)
+  *c = __uint_as_float(__float_as_uint((odd ? sa : ca) * scale) ^ (((quarter + 1u) & 2u) << 30));
+  *s = __uint_as_float(__float_as_uint((odd ? ca : sa) * scale) ^ ((quarter & 2u) << 30));
 }
 
 // Which eight of a head's 128 values lane i of 16 takes: [lo, lo + 4) and [hi,
@@ -283,12 +292,12 @@ __device__ __forceinline__ void kv8_rotate_q(const Kv8AppendArgs& a, int64_t cap
 // first code.
 //
 // HBM-bound (2 bytes read per value, 2 or 1 written) for many rows: 8200 tokens,
-// 32 + 2 x 8 heads, 184 MB, 37 us (5.0 TB/s); the rows of q alone run at 5.5
+// 32 + 2 x 8 heads, 184 MB, 41 us (4.5 TB/s); the rows of q alone run at 5.5
 // TB/s, the pages are held up by the chain of reads in front of theirs (length,
-// start, page). A decode step is that chain: 16 sequences 2.2 us. All of a thread's
+// start, page). A decode step is that chain: 16 sequences 2.3 us. All of a thread's
 // reads are under way before the angles are worked out, and a page's angles by
 // the thread that rotates with them: sharing them among a block's threads
-// through shared memory took a barrier a slab and 42 us.
+// through shared memory took a barrier a slab and 5 us more.
 //
 // PAGE: the page's tokens; 0: one new token per sequence in pages of any size,
 // by the one slab that holds it. Measured, 64 such sequences, pages of 16 / 32 /
@@ -383,9 +392,20 @@ __global__ void __launch_bounds__(kv8_append_threads(PAGE), kv8_append_blocks(PA
   for (int p = 0; p < kPasses; ++p) {
     const int j = slab0 + p * kSlab + (t >> 4);
     if (j >= lo && j < hi) {
-      // (|x| r <= 127 (1 + 2^-22): no code is beyond 127)
-      *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.lo) = pack_codes(x[p], r);
-      *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.hi) = pack_codes(x[p] + 4, r);
+      // x / s' by the reciprocal, then corrected by its remainder (Markstein 1990,
+      // "Computation of elementary functions on the IBM RISC System/6000
+      // processor"): a quotient midway between two codes (x = 3 at a scale of 6,
+      // half the page's largest value) comes out as that and goes to the even one;
+      // x * (1 / s') alone lands on either side. 1.5 us of 41, an IEEE division 7.
+      float u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float q = x[p][e] * r;
+        u[e] = fmaf(fmaf(-q, s_new, x[p][e]), r, q);
+      }
+      // (|u| <= 127 (1 + 2^-22): no code is beyond 127)
+      *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.lo) = pack_codes(u, 1.0f);
+      *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.hi) = pack_codes(u + 4, 1.0f);
     }
   }
   if (lo > 0 && s_new > s_old) {  // the codes that were there, carried over to the larger scale
