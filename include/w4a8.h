@@ -542,8 +542,8 @@ typedef struct {
  * j, 2 j + 1) if interleaved, else (j, j + rotary_dim / 2),
  *   (a, b) -> rope_scale * (a cos t - b sin t, a sin t + b cos t),  t = p * inv_freq[j],
  * the angle exact to 2^-22 radians at every position (no fp32 product of a
- * large position), its sine and cosine to 2^-20. inv_freq: fp32 [rotary_dim / 2] in device memory, as scaled
- * for long contexts by the caller; rope_scale: a factor on the rotated values
+ * large position), its sine and cosine to 2^-23. inv_freq: fp32 [rotary_dim /
+ * 2] in device memory, as scaled for long contexts by the caller; rope_scale: a factor on the rotated values
  * (1 for none).
  * q goes to q_out, fp16 [T, Hq, 128] (16-byte aligned, no part of qkv); k and v (as fp32, not
  * rounded in between) into the cache. In every page that gets new tokens

@@ -102,7 +102,7 @@ __host__ __device__ constexpr int kv8_append_blocks(int P) { return P <= 32 ? 8 
 // below 2^-25. The sine and cosine come out within 2^-23, so that an
 // angle moves a code by 127 * 2^-23 of a step and few lie that near the middle
 // between two. (The hardware's approximations, within 2^-20.5, took 37.1 us
-// where these take 39.6: six times as many codes go to the farther of two.)
+// where these take 39.6, with an error bound six times as wide.)
 __device__ __forceinline__ uint64_t kv8_turns(float f) {
   const double t = static_cast<double>(f) * 0.15915494309189533577;  // 1 / (2 pi)
   return static_cast<uint64_t>((t - floor(t)) * 18446744073709551616.0);
