@@ -357,7 +357,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8PrefillA
       }
       give(j, mx);
       // O and P are this block's again once the last tile's product is done
-      if (j > 0 && !(ok = wait_warp(kPFree + blk, j - 1))) break;
+      if (j > 0) {
+        if (!(ok = wait_warp(kPFree + blk, j - 1))) break;
+        tc_fence_after();  // of P's stores below too, in tiles that leave O as it is
+      }
       mx = fmaxf(mx, take(j, ok));
       if (!ok) break;
       // move the reference where the maximum has passed it
@@ -367,7 +370,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8PrefillA
         ref = move ? mx : ref;
         l *= f;
         if (j > 0) {
-          tc_fence_after();
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             uint32_t o[16];
