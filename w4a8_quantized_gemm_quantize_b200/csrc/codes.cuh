@@ -13,4 +13,14 @@ __device__ __forceinline__ uint32_t pack_codes(const float* v, float inv) {
   return __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
 }
 
+// x / s for r = 1 / s (IEEE): the product by the reciprocal, corrected by its
+// remainder (Markstein 1990, "Computation of elementary functions on the IBM
+// RISC System/6000 processor"). A quotient midway between two codes comes out
+// as that, and goes to the even one; x * r alone lands on either side. (r = 0
+// gives 0.)
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, s, x), r, q);
+}
+
 }  // namespace w4a8

@@ -4,7 +4,7 @@
 // rstd = 1 / sqrt(mean(h^2) + eps) (fp32, IEEE square root and divide), then
 // the per-token quantization of quantize_act.cuh on the fp32 values of y (no
 // rounding to fp16 in between): sA = fp16_rn(max |y| / 127), A8 =
-// clamp(rint(y * (1 / sA)), -127, 127), rowsum = sum A8. What w4a8_gemm takes, so
+// clamp(rint(y / sA), -127, 127), rowsum = sum A8. What w4a8_gemm takes, so
 // that the norm in front of a linear layer ("QServe/QoQ" abstract: W4A8
 // serving) costs one read of its input instead of a write and two reads more.
 //
@@ -41,9 +41,10 @@ __device__ __forceinline__ float block_all(float v, float* red) {
 // weights and y stay in registers too; with 8 vectors a thread and 1024 threads
 // (64 registers each) only the row does, and y is worked out twice.
 //
-// Measured, device time: 8192 x 4096 with residual 38.5 us (6.1 TB/s), 1024 x
-// 14336 20 us (5.1 TB/s; with 512 threads of 4 vectors 25: more vectors a thread
-// keep more of the row under way), 1 x 4096 1.9 us.
+// Measured, replayed graphs: 8192 x 4096 with residual 39.0 us (6.0 TB/s), 1024 x
+// 14336 17.7 us (its 103 MB partly in L2; with 512 threads of 4 vectors a quarter
+// more: more vectors a thread keep more of the row under way), 1 x 4096 2.0 us. The
+// codes' quotients corrected by their remainder cost 0.8 of the 39.0.
 template <int THREADS, int VPT, bool RES>
 __global__ void __launch_bounds__(THREADS) rmsnorm_quantize_kernel(const __half* X, const __half* R,
                                                                    const __half* __restrict__ W, float eps,
@@ -147,7 +148,9 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_quantize_kernel(const __half*
       for (int e = 0; e < 8; ++e) yy[e] = fminf(fmaxf(yy[e], -top), top);
     }
     if (idx < nvec) {
-      const uint2 c = make_uint2(pack_codes(yy, inv), pack_codes(yy + 4, inv));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) yy[e] = quotient(yy[e], sf, inv);
+      const uint2 c = make_uint2(pack_codes(yy, 1.0f), pack_codes(yy + 4, 1.0f));
       reinterpret_cast<uint2*>(A8 + m * K)[idx] = c;
       local = __dp4a(static_cast<int>(c.x), 0x01010101, local);
       local = __dp4a(static_cast<int>(c.y), 0x01010101, local);
