@@ -486,7 +486,7 @@ W4A8_API w4a8_status_t w4kv_attention_decode(const void* q, const uint8_t* k_cod
  * ("QServe/QoQ" abstract: W4A8 serving). For each row m:
  *   h[m,k] = fp16_rn(X[m,k] + residual[m,k])   (h = X without a residual)
  *   y[m,k] = h[m,k] * (1 / sqrt(mean_k h[m,k]^2 + eps)) * weight[k]   (fp32)
- *   sA[m]  = fp16_rn(max_k |y[m,k]| / 127)
+ *   sA[m]  = fp16_rn(min(max_k |y[m,k]| / 127, 65504))   (large weights: y up to 256 * 65504)
  *   A8[m,k] = clamp(rint(y[m,k] / float(sA[m])), -127, 127)   (ties to even)
  *   sA[m] == 0 gives A8[m,:] = 0;  rowsum[m] = sum_k A8[m,k].
  * (A8, sA, rowsum) feed w4a8_gemm as those of w4a8_quantize_act do. The

@@ -59,3 +59,16 @@ def test_quotients_midway_between_two_codes_go_to_the_even_one(K):
     assert float(s[0]) == 3.0 / 64 and (codes[0].cpu().numpy() == want).all() and int(rowsum[0]) == int(want.sum())
     plain, s2, rowsum2 = w4a8.quantize_act(dev((sign * w)[None].astype(np.float16)))
     assert torch.equal(codes, plain) and torch.equal(s, s2) and torch.equal(rowsum, rowsum2)
+
+
+@pytest.mark.parametrize("K", [16384, 65536])
+def test_a_scale_beyond_fp16_is_its_largest_value(K):
+    """One value alone in a wide row, under the largest weight: y = sqrt(K) *
+    65504 is more than 127 * 65504; sA is 65504 and the code 127, none infinite."""
+    x = np.zeros((2, K), np.float16)
+    x[0, 3], x[1, K - 1] = 1.0, -2.0
+    w = np.full(K, 65504.0, np.float16)
+    _, codes, s, rowsum = w4a8.rmsnorm_quantize_act(dev(x), dev(w), 0.0)
+    assert (s == 65504).all()
+    assert int(codes[0, 3]) == 127 and int(codes[1, K - 1]) == -127 and rowsum.tolist() == [127, -127]
+    assert int((codes != 0).sum()) == 2

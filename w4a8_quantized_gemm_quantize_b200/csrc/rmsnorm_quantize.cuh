@@ -3,7 +3,7 @@
 // Row m: h = fp16_rn(x + r) (h = x without a residual), y = h * rstd * w with
 // rstd = 1 / sqrt(mean(h^2) + eps) (fp32, IEEE square root and divide), then
 // the per-token quantization of quantize_act.cuh on the fp32 values of y (no
-// rounding to fp16 in between): sA = fp16_rn(max |y| / 127), A8 =
+// rounding to fp16 in between): sA = fp16_rn(min(max |y| / 127, 65504)), A8 =
 // clamp(rint(y / sA), -127, 127), rowsum = sum A8. What w4a8_gemm takes, so
 // that the norm in front of a linear layer ("QServe/QoQ" abstract: W4A8
 // serving) costs one read of its input instead of a write and two reads more.
@@ -130,12 +130,12 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_quantize_kernel(const __half*
     for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(yy[e]));
   }
   amax = block_all<THREADS, true>(amax, s_max);
-  const __half s_h = __float2half_rn(__fdiv_rn(amax, 127.0f));
+  const __half s_h = __float2half_rn(fminf(__fdiv_rn(amax, 127.0f), 65504.0f));
   const float sf = __half2float(s_h);
   const float inv = sf > 0.0f ? __fdiv_rn(1.0f, sf) : 0.0f;
   // A normal scale is within 2^-11 of amax / 127, so that no code passes 127;
-  // a subnormal one may be half of it.
-  const bool clamp = sf < 6.2e-5f;
+  // a subnormal one may be half of it, and the largest stands for all beyond it.
+  const bool clamp = sf < 6.2e-5f || sf == 65504.0f;
   const float top = 127.0f * sf;
   int local = 0;
 #pragma unroll
