@@ -541,7 +541,7 @@ typedef struct {
  * head are rotated by the token's position p = seq_lens[b] - n_b + i: pairs (2
  * j, 2 j + 1) if interleaved, else (j, j + rotary_dim / 2),
  *   (a, b) -> rope_scale * (a cos t - b sin t, a sin t + b cos t),  t = p * inv_freq[j],
- * the angle exact to 2^-22 radians at every position (no fp32 product of a
+ * the angle exact to 2^-22 radians at every position and for |inv_freq[j]| up to 2^30 (no fp32 product of a
  * large position), its sine and cosine to 2^-23. inv_freq: fp32 [rotary_dim /
  * 2] in device memory, as scaled for long contexts by the caller; rope_scale: a factor on the rotated values
  * (1 for none).

@@ -104,8 +104,12 @@ __host__ __device__ constexpr int kv8_append_blocks(int P) { return P <= 32 ? 8 
 // between two. (The hardware's approximations, within 2^-20.5, took 37.1 us
 // where these take 39.6, with an error bound six times as wide.)
 __device__ __forceinline__ uint64_t kv8_turns(float f) {
-  const double t = static_cast<double>(f) * 0.15915494309189533577;  // 1 / (2 pi)
-  return static_cast<uint64_t>((t - floor(t)) * 18446744073709551616.0);
+  // 1 / (2 pi) in two terms, and the first product's remainder: what is left of
+  // whole turns is within 2^-54 for a frequency of any size
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
+  const double x = static_cast<double>(f), t = x * kHi;
+  const double part = (t - rint(t)) + fma(x, kLo, fma(x, kHi, -t));
+  return static_cast<uint64_t>(__double2ll_rn(part * 18446744073709551616.0));
 }
 __device__ __forceinline__ void kv8_cos_sin(uint64_t turns, int pos, float scale, float* c, float* s) {
   const uint32_t top = static_cast<uint32_t>((turns * static_cast<uint64_t>(pos)) >> 32);
