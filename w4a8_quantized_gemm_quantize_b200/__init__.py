@@ -848,13 +848,22 @@ def kv8_workspace_bytes(B: int, T: int, Hq: int, Hkv: int) -> int:
 _kv8_ws = {}
 
 
+def _capturing(index) -> bool:
+    """Whether the current stream of CUDA device `index` is being captured (torch asks the current device's)."""
+    torch = _torch()
+    if torch.cuda.current_device() == index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(index):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _kv8_workspace_for(q, index, B, T, Hq, Hkv):
     """A zero-filled workspace per stream (calls on different streams may
     overlap), grown on demand and reused; a call that is being captured gets
     one of its own, which its graph zero-fills and keeps."""
     torch = _torch()
     nbytes = max(kv8_workspace_bytes(B, T, Hq, Hkv), 256)
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing(index):
         return torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
     key = (index, torch._C._cuda_getCurrentRawStream(index))
     ws = _kv8_ws.get(key)
