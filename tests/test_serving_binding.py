@@ -51,3 +51,28 @@ def test_a_captured_call_is_that_of_the_tensors_device(monkeypatch, current, ind
     a = f.workspace(index)
     assert (f.workspace(index) is a) == kept and bool(w4a8._kv8_ws) == kept
     assert f.current == current
+
+
+@pytest.mark.parametrize("device", [None, 0, "cuda:0", "cuda"])
+def test_a_cleared_device_error_begins_with_new_workspaces(monkeypatch, device):
+    """A wait that gave up leaves counters that would have later calls join too
+    early: clearing the error lets every stream's kept workspace of that device go."""
+    f = FakeCuda(monkeypatch)
+
+    class Lib:
+        def w4a8_clear_device_error(self, stream):
+            return 0
+
+    a, other = f.workspace(0), f.workspace(1)
+    f.streams[0] = 101
+    b = f.workspace(0)
+    for ws in (a, b, other):
+        ws[:64] = 1  # arrivals of a call that gave up
+    with monkeypatch.context() as m:
+        m.setattr(w4a8, "lib", Lib)
+        m.setattr(w4a8, "_stream", lambda d: None)
+        w4a8.clear_device_error(torch.device(device) if device == "cuda:0" else device)
+    again = f.workspace(0)
+    f.streams[0] = 100
+    assert not again.any() and not f.workspace(0).any()
+    assert f.workspace(1) is other  # another device's is its own

@@ -538,7 +538,16 @@ def get_device_error(device=None) -> int:
 
 
 def clear_device_error(device=None):
+    """Clears the error word. A call that gave up may have left its workspace's
+    counters above zero: those kept here for the KV8 attention are let go, and
+    the next calls begin with new ones (a workspace of the caller's own is the
+    caller's to zero-fill)."""
+    torch = _torch()
     _check(lib().w4a8_clear_device_error(_stream(device)), "w4a8_clear_device_error")
+    index = None if device is None else torch.device(device).index
+    index = torch.cuda.current_device() if index is None else index
+    for key in [k for k in _kv8_ws if k[0] == index]:
+        del _kv8_ws[key]
 
 
 DEVERR_SELFTEST_WAIT = 6
@@ -546,6 +555,7 @@ DEVERR_KV_RANGE = 7
 DEVERR_PACK_RANGE = 8
 DEVERR_CHAIN_WAIT = 9
 DEVERR_BOUNDS = 10
+DEVERR_KV_WAIT = 11
 
 
 def selftest_bounded_wait(limit_ns: int, device=None):
