@@ -102,11 +102,12 @@ w4a8_status_t launch_kv8_decode(const CUtensorMap& map, const Kv8DecodeArgs& d, 
 // heads (decode against prefill kernel): 1 sequence of 32 rows over 1000, 4000,
 // 32000 tokens 14, 24, 67 us against 23, 26, 55; of 64 rows 19, 29, 114 against
 // 24, 26, 56; 4 sequences of 32 rows over 1000, 4000 tokens 22, 43 against 25,
-// 37. Where several sequences have 160 rows in all, as many short guesses do,
-// all go to the decode kernel: the others' launches would do nothing for 5 us.
-int kv8_few_rows(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
-  return B > 1 && T * (Hq / Hkv) <= 160 ? 160 : 32;
-}
+// 37. Each sequence by its own rows, whatever the batch's. With batches of up to
+// 160 rows given to the decode kernel whole, 156 rows over 1000, 8000, 32000
+// tokens beside one of 4 over 500 took 24, 78, 262 us, now 40, 53, 110; 8
+// sequences of 20 rows over 1500, for which the other kernel has nothing to do, 29,
+// now 35.
+constexpr int kKv8FewRows = 32;
 
 w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_cache_t* c, void* workspace,
                          cudaStream_t stream) {
@@ -118,7 +119,7 @@ w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_c
   d.a = a;
   d.count = static_cast<int*>(workspace);
   d.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kDecMaxCtas * 4);
-  d.max_rows = a.s.q_start == nullptr ? G : kv8_few_rows(a.s.B, a.s.T, a.Hq, a.c.Hkv);
+  d.max_rows = a.s.q_start == nullptr ? G : kKv8FewRows;
   // one CTA per SM, no more than the longest possible batch has tiles for
   const int64_t tiles = (c->max_blocks * c->page + kDecTile - 1) / kDecTile * a.s.B * a.c.Hkv *
                         ((d.max_rows + kDecCols - 1) / kDecCols);
@@ -137,7 +138,7 @@ int kv8_pre_splits(int64_t slots, int64_t Hkv) {
   return static_cast<int>(n < 2 ? 1 : n > 32 ? 32 : n);
 }
 size_t kv8_pre_part_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
-  if (T * (Hq / Hkv) <= kv8_few_rows(B, T, Hq, Hkv)) return 0;
+  if (T * (Hq / Hkv) <= kKv8FewRows) return 0;
   const int64_t slots = kv8_pre_slots(B, T, Hq / Hkv);
   const int splits = kv8_pre_splits(slots, Hkv);
   return splits > 1 ? static_cast<size_t>(slots * Hkv * splits) * (2 * kPreRows) * (kKv8D + 2) * 4 : 0;
@@ -204,11 +205,10 @@ w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int3
   // each kernel takes the sequences that suit it; one whose share must be
   // empty is not launched
   const int64_t rows = T * (Hq / c->Hkv);
-  const int few = kv8_few_rows(B, T, Hq, c->Hkv);
-  if (rows <= few) return kv8_decode(a, dev, c, workspace, stream);
+  if (rows <= kKv8FewRows) return kv8_decode(a, dev, c, workspace, stream);
   if (B == 1) return kv8_prefill(a, 0, workspace, stream);
   st = kv8_decode(a, dev, c, workspace, stream);
-  return st != W4A8_OK ? st : kv8_prefill(a, few, workspace, stream);
+  return st != W4A8_OK ? st : kv8_prefill(a, kKv8FewRows, workspace, stream);
 }
 
 }  // namespace
