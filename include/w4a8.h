@@ -561,8 +561,12 @@ W4A8_API w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cach
                                             float rope_scale, void* q_out, w4a8_stream_t stream);
 
 /* Workspace bytes of the attention calls below (0 if the sizes are
- * unsupported); it does not depend on the lengths. */
+ * unsupported), whatever the lengths: of every call of at most B sequences and
+ * T rows (it does not fall as B or T grow), and of a decode call of at most B
+ * sequences, which needs less. */
+#define W4A8_KV8_COUNTER_BYTES 1024 /* a workspace's first bytes: counters, zero between calls */
 W4A8_API size_t w4a8_kv8_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv);
+W4A8_API size_t w4a8_kv8_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv);
 
 /*
  * Attention of one new token per sequence over the cache that already holds
@@ -571,10 +575,11 @@ W4A8_API size_t w4a8_kv8_attention_workspace_bytes(int64_t B, int64_t T, int64_t
  *   s_j = scale * sK * sum_d q[d] * codeK[j, d],  j < seq_lens[b]
  *   out[b, h] = fp16_rn(sum_j softmax(s)_j * sV * codeV[j])
  * with sK, sV the scales of j's page, in fp32; seq_lens[b] == 0 gives zeros.
- * workspace: 256-byte aligned, at least w4a8_kv8_attention_workspace_bytes(B,
- * B, Hq, Hkv) bytes, zero-filled by the caller once; every call that completes
- * without a device error leaves its counters zero again. Calls that share a
- * workspace must not overlap on the GPU.
+ * workspace: 256-byte aligned, at least w4a8_kv8_decode_workspace_bytes(B, Hq,
+ * Hkv) bytes, its first W4A8_KV8_COUNTER_BYTES zero-filled by the caller once;
+ * every call that completes without a device error leaves them zero again (after
+ * one, the caller zero-fills them once more). Calls that share a workspace must
+ * not overlap on the GPU.
  */
 W4A8_API w4a8_status_t w4a8_kv8_attention_decode(const void* q, const w4a8_kv8_cache_t* cache,
                                                  const int32_t* seq_lens, int64_t B, int64_t Hq, float scale,
@@ -586,7 +591,7 @@ W4A8_API w4a8_status_t w4a8_kv8_attention_decode(const void* q, const w4a8_kv8_c
  * causal: row i of sequence b's n_b rows sees its tokens j < seq_lens[b] - n_b
  * + i + 1. q, out: fp16 [T, Hq, 128] (out may be q). The softmax weights are
  * rounded to fp16 for the product with the values, their sum is not. workspace as for the decode call, of
- * w4a8_kv8_attention_workspace_bytes(B, T, Hq, Hkv) bytes.
+ * w4a8_kv8_attention_workspace_bytes(B, T, Hq, Hkv) bytes; calls of both kinds may share one.
  */
 W4A8_API w4a8_status_t w4a8_kv8_attention_prefill(const void* q, const w4a8_kv8_cache_t* cache,
                                                   const int32_t* seq_lens, const int32_t* q_start, int64_t B,

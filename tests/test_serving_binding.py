@@ -31,8 +31,8 @@ class FakeCuda:
         finally:
             self.current = saved
 
-    def workspace(self, index, B=2, T=2, Hq=8, Hkv=2):
-        return w4a8._kv8_workspace_for(self.q, index, B, T, Hq, Hkv)
+    def workspace(self, index, nbytes=4096):
+        return w4a8._kv8_workspace_for(self.q, index, nbytes)
 
 
 def test_a_workspace_is_kept_for_each_stream(monkeypatch):

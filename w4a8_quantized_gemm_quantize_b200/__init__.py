@@ -23,7 +23,8 @@ __all__ = [
     "w4a4_gemm", "w4a4_gemm_ex", "w4a4_workspace_bytes", "lut_packed_bytes", "lut_pack_weights", "lut_gemm",
     "lut_gemm_ex", "lut3_packed_bytes", "lut3_pack_weights", "lut3_gemm", "lut3_gemm_ex", "kv4_quantize", "kv4_append", "kv4_workspace_bytes", "kv4_attention_decode",
     "ChainLink", "chain_links", "chain_workspace_bytes", "chain", "rmsnorm_quantize_act", "kv8_cache",
-    "rope_frequencies", "kv8_rope_append", "kv8_workspace_bytes", "kv8_attention_decode", "kv8_attention_prefill",
+    "rope_frequencies", "kv8_rope_append", "kv8_workspace_bytes", "kv8_decode_workspace_bytes", "kv8_attention_decode",
+    "kv8_attention_prefill",
 ]
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -40,7 +41,7 @@ EXPORTED_SYMBOLS = (
     "w4lut3_packed_bytes", "w4lut3_pack_weights", "w4lut3_gemm", "w4lut3_gemm_ex",
     "w4a8_chain_workspace_bytes", "w4a8_chain",
     "w4a8_rmsnorm_quantize_act", "w4a8_kv8_rope_append", "w4a8_kv8_attention_workspace_bytes",
-    "w4a8_kv8_attention_decode", "w4a8_kv8_attention_prefill",
+    "w4a8_kv8_decode_workspace_bytes", "w4a8_kv8_attention_decode", "w4a8_kv8_attention_prefill",
 )
 
 SCHEDULE_AUTO, SCHEDULE_WHOLE_TILES, SCHEDULE_SPLIT_K, SCHEDULE_CLUSTER = 0, 1, 2, 3
@@ -124,6 +125,7 @@ def lib() -> ctypes.CDLL:
         "w4a8_kv8_rope_append": (ctypes.c_int, [vp, ctypes.POINTER(Kv8CacheDesc), vp, vp, i64, i64, i64, vp, i32, i32,
                                                 ctypes.c_float, vp, vp]),
         "w4a8_kv8_attention_workspace_bytes": (sz, [i64, i64, i64, i64]),
+        "w4a8_kv8_decode_workspace_bytes": (sz, [i64, i64, i64]),
         "w4a8_kv8_attention_decode": (ctypes.c_int, [vp, ctypes.POINTER(Kv8CacheDesc), vp, i64, i64, ctypes.c_float,
                                                      vp, vp, sz, vp]),
         "w4a8_kv8_attention_prefill": (ctypes.c_int, [vp, ctypes.POINTER(Kv8CacheDesc), vp, vp, i64, i64, i64,
@@ -852,8 +854,16 @@ def kv8_rope_append(qkv, Hq: int, kv_codes, kv_scales, block_table, seq_lens, in
 
 
 def kv8_workspace_bytes(B: int, T: int, Hq: int, Hkv: int) -> int:
+    """Of every attention call of at most B sequences and T rows."""
     return int(lib().w4a8_kv8_attention_workspace_bytes(B, T, Hq, Hkv))
 
+
+def kv8_decode_workspace_bytes(B: int, Hq: int, Hkv: int) -> int:
+    """Of a decode call of at most B sequences."""
+    return int(lib().w4a8_kv8_decode_workspace_bytes(B, Hq, Hkv))
+
+
+KV8_COUNTER_BYTES = 1024  # W4A8_KV8_COUNTER_BYTES: the first bytes of a workspace, zero between calls
 
 _kv8_ws = {}
 
@@ -867,12 +877,12 @@ def _capturing(index) -> bool:
         return torch.cuda.is_current_stream_capturing()
 
 
-def _kv8_workspace_for(q, index, B, T, Hq, Hkv):
+def _kv8_workspace_for(q, index, nbytes):
     """A zero-filled workspace per stream (calls on different streams may
     overlap), grown on demand and reused; a call that is being captured gets
     one of its own, which its graph zero-fills and keeps."""
     torch = _torch()
-    nbytes = max(kv8_workspace_bytes(B, T, Hq, Hkv), 256)
+    nbytes = max(nbytes, 256)
     if _capturing(index):
         return torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
     key = (index, torch._C._cuda_getCurrentRawStream(index))
@@ -896,7 +906,8 @@ def _kv8_attention(what, q, kv_codes, kv_scales, block_table, seq_lens, scale, q
     else:
         _check_tensor(out, "out", f16, dev, shape)
     if workspace is None:
-        workspace = _kv8_workspace_for(q, dev, B, T, Hq, Hkv)
+        workspace = _kv8_workspace_for(q, dev, kv8_decode_workspace_bytes(B, Hq, Hkv) if q_start is None
+                                       else kv8_workspace_bytes(B, T, Hq, Hkv))
     else:
         _check_tensor(workspace, "workspace", torch.uint8, dev)
     L = lib()
@@ -913,7 +924,7 @@ def _kv8_attention(what, q, kv_codes, kv_scales, block_table, seq_lens, scale, q
 def kv8_attention_decode(q, kv_codes, kv_scales, block_table, seq_lens, scale, out=None, workspace=None):
     """Attention of one new token per sequence, q fp16 [B, Hq, 128], over the
     paged 8-bit cache that holds it (seq_lens int32 [B]) -> fp16 [B, Hq, 128].
-    workspace: zero-filled uint8 of kv8_workspace_bytes(B, B, Hq, Hkv) (one
+    workspace: zero-filled uint8 of kv8_decode_workspace_bytes(B, Hq, Hkv) (one
     per stream is kept here if none is given); calls that share it must not
     overlap on the GPU."""
     return _kv8_attention("w4a8_kv8_attention_decode", q, kv_codes, kv_scales, block_table, seq_lens, scale, None,

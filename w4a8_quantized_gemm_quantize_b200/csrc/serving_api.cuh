@@ -137,13 +137,28 @@ int kv8_pre_splits(int64_t slots, int64_t Hkv) {
   const int64_t n = 148 / (slots * Hkv);
   return static_cast<int>(n < 2 ? 1 : n > 32 ? 32 : n);
 }
+size_t kv8_part_bytes(int64_t parts) { return static_cast<size_t>(parts) * (2 * kPreRows) * (kKv8D + 2) * 4; }
+// What the parts of a call take, and the most that those of any call of at most B
+// sequences and T rows do (fewer pieces are cut into more parts).
 size_t kv8_pre_part_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
   if (T * (Hq / Hkv) <= kKv8FewRows) return 0;
   const int64_t slots = kv8_pre_slots(B, T, Hq / Hkv);
   const int splits = kv8_pre_splits(slots, Hkv);
-  return splits > 1 ? static_cast<size_t>(slots * Hkv * splits) * (2 * kPreRows) * (kKv8D + 2) * 4 : 0;
+  return splits > 1 ? kv8_part_bytes(slots * Hkv * splits) : 0;
+}
+size_t kv8_most_part_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
+  if (T * (Hq / Hkv) <= kKv8FewRows) return 0;
+  const int64_t slots = kv8_pre_slots(B, T, Hq / Hkv);
+  int64_t most = 0;
+  for (int64_t n = 1; n <= slots; ++n) {  // (148 / 2 at most)
+    const int splits = kv8_pre_splits(n, Hkv);
+    if (splits == 1) break;
+    most = n * Hkv * splits > most ? n * Hkv * splits : most;
+  }
+  return kv8_part_bytes(most);
 }
 constexpr size_t kDecWorkspace = kDecMaxCtas * (4 + 2 * kDecPart * sizeof(float));
+static_assert(kDecMaxCtas * 4 == W4A8_KV8_COUNTER_BYTES, "the counters come first");
 static_assert(kDecWorkspace % 256 == 0, "the prefill parts follow, aligned");
 
 template <bool CUT>
@@ -188,8 +203,8 @@ w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int3
   if (st != W4A8_OK) return st;
   if (q == nullptr || out == nullptr) return W4A8_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return W4A8_ERR_MISALIGNED;
-  if (workspace == nullptr || workspace_bytes < w4a8_kv8_attention_workspace_bytes(B, T, Hq, c->Hkv))
-    return W4A8_ERR_WORKSPACE;
+  const size_t parts = q_start == nullptr ? 0 : kv8_pre_part_bytes(B, T, Hq, c->Hkv);
+  if (workspace == nullptr || workspace_bytes < kDecWorkspace + parts) return W4A8_ERR_WORKSPACE;
   DeviceInfo* dev = nullptr;
   st = device_info(&dev);
   if (st != W4A8_OK) return st;
@@ -282,7 +297,11 @@ w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cache_t* cach
 size_t w4a8_kv8_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv) {
   if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || B > 65535 || T > INT32_MAX / 1024 || Hq > 1024)
     return 0;
-  return kDecWorkspace + kv8_pre_part_bytes(B, T, Hq, Hkv);
+  return kDecWorkspace + kv8_most_part_bytes(B, T, Hq, Hkv);
+}
+
+size_t w4a8_kv8_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv) {
+  return w4a8_kv8_attention_workspace_bytes(B, B, Hq, Hkv) != 0 ? kDecWorkspace : 0;
 }
 
 w4a8_status_t w4a8_kv8_attention_decode(const void* q, const w4a8_kv8_cache_t* cache, const int32_t* seq_lens,
