@@ -38,7 +38,7 @@ class FakeCuda:
 def test_a_workspace_is_kept_for_each_stream(monkeypatch):
     f = FakeCuda(monkeypatch)
     a = f.workspace(0)
-    assert f.workspace(0) is a and not a.any()
+    assert f.workspace(0) is a and not a[:w4a8.KV8_COUNTER_BYTES].any()
     f.streams[0] = 101
     assert f.workspace(0) is not a
 
@@ -74,5 +74,26 @@ def test_a_cleared_device_error_begins_with_new_workspaces(monkeypatch, device):
         w4a8.clear_device_error(torch.device(device) if device == "cuda:0" else device)
     again = f.workspace(0)
     f.streams[0] = 100
-    assert not again.any() and not f.workspace(0).any()
+    assert not again[:64].any() and not f.workspace(0)[:64].any()
     assert f.workspace(1) is other  # another device's is its own
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_no_more_than_the_counters_is_filled(monkeypatch, capturing):
+    """A captured call fills its workspace at every replay: 1 KiB of it, not the
+    megabytes of partial results behind."""
+    f = FakeCuda(monkeypatch, 0, {0} if capturing else ())
+    made = []
+
+    def empty(n, **kw):
+        made.append(torch.full((n,), 0x7F, **kw))
+        return made[-1]
+
+    def zeros(*a, **kw):
+        raise AssertionError("the whole workspace is filled")
+    with monkeypatch.context() as m:
+        m.setattr(torch, "empty", empty)
+        m.setattr(torch, "zeros", zeros)
+        ws = f.workspace(0, 1 << 16)
+    n = w4a8.KV8_COUNTER_BYTES
+    assert ws is made[0] and not ws[:n].any() and bool((ws[n:] == 0x7F).all())

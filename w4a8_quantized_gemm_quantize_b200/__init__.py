@@ -878,17 +878,18 @@ def _capturing(index) -> bool:
 
 
 def _kv8_workspace_for(q, index, nbytes):
-    """A zero-filled workspace per stream (calls on different streams may
-    overlap), grown on demand and reused; a call that is being captured gets
-    one of its own, which its graph zero-fills and keeps."""
+    """A workspace per stream (calls on different streams may overlap), grown on
+    demand and reused; a call that is being captured gets one of its own, which
+    its graph keeps. Each replay zero-fills its counters, and no more."""
     torch = _torch()
-    nbytes = max(nbytes, 256)
-    if _capturing(index):
-        return torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
+    capturing = _capturing(index)
     key = (index, torch._C._cuda_getCurrentRawStream(index))
-    ws = _kv8_ws.get(key)
+    ws = None if capturing else _kv8_ws.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = _kv8_ws[key] = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
+        ws = torch.empty(max(nbytes, KV8_COUNTER_BYTES), dtype=torch.uint8, device=q.device)
+        ws[:KV8_COUNTER_BYTES].zero_()
+        if not capturing:
+            _kv8_ws[key] = ws
     return ws
 
 
@@ -924,9 +925,9 @@ def _kv8_attention(what, q, kv_codes, kv_scales, block_table, seq_lens, scale, q
 def kv8_attention_decode(q, kv_codes, kv_scales, block_table, seq_lens, scale, out=None, workspace=None):
     """Attention of one new token per sequence, q fp16 [B, Hq, 128], over the
     paged 8-bit cache that holds it (seq_lens int32 [B]) -> fp16 [B, Hq, 128].
-    workspace: zero-filled uint8 of kv8_decode_workspace_bytes(B, Hq, Hkv) (one
-    per stream is kept here if none is given); calls that share it must not
-    overlap on the GPU."""
+    workspace: uint8 of kv8_decode_workspace_bytes(B, Hq, Hkv), its first
+    KV8_COUNTER_BYTES zero (one per stream is kept here if none is given); calls
+    that share it must not overlap on the GPU."""
     return _kv8_attention("w4a8_kv8_attention_decode", q, kv_codes, kv_scales, block_table, seq_lens, scale, None,
                           out, workspace)
 
