@@ -57,7 +57,7 @@ typedef struct CUstream_st* w4a8_stream_t;
 
 typedef enum {
   W4A8_OK = 0,
-  W4A8_ERR_INVALID_ARG = 1,       /* null pointer, negative size, bad option */
+  W4A8_ERR_INVALID_ARG = 1,       /* null pointer, negative size, bad option, buffers that overlap */
   W4A8_ERR_UNSUPPORTED_SHAPE = 2, /* shape outside the documented limits */
   W4A8_ERR_MISALIGNED = 3,        /* pointer not aligned as required */
   W4A8_ERR_WORKSPACE = 4,         /* workspace missing or too small */
@@ -493,7 +493,8 @@ W4A8_API w4a8_status_t w4kv_attention_decode(const void* q, const uint8_t* k_cod
  * quantizer works on the fp32 values of y; the norm on the rounded h, so that
  * a call on h alone gives the same codes.
  * X, residual: fp16 [M, K] (16-byte aligned); residual may be NULL, and H is
- * NULL exactly then. H: fp16 [M, K], h; it may be X or residual itself.
+ * NULL exactly then. H: fp16 [M, K], h; it may be X or residual itself, but no
+ * other part of them (W4A8_ERR_INVALID_ARG).
  * weight: fp16 [K] (16-byte aligned). eps >= 0. A8, sA, rowsum and the limits
  * as for w4a8_quantize_act. Non-finite inputs, or an h beyond fp16, are a
  * precondition violation (that row's codes unspecified).
@@ -545,7 +546,7 @@ typedef struct {
  * large position), its sine and cosine to 2^-23. inv_freq: fp32 [rotary_dim /
  * 2] in device memory, as scaled for long contexts by the caller; rope_scale: a factor on the rotated values
  * (1 for none).
- * q goes to q_out, fp16 [T, Hq, 128] (16-byte aligned, no part of qkv); k and v (as fp32, not
+ * q goes to q_out, fp16 [T, Hq, 128] (16-byte aligned, no part of qkv: W4A8_ERR_INVALID_ARG); k and v (as fp32, not
  * rounded in between) into the cache. In every page that gets new tokens
  *   s' = max(s, fp32(max |new values| / 127)),  s = 0 if the page's first place is one of them
  *   codes that were there: rint(code * (s / s')) if s' > s
@@ -570,7 +571,7 @@ W4A8_API size_t w4a8_kv8_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t H
 
 /*
  * Attention of one new token per sequence over the cache that already holds
- * it. q, out: fp16 [B, Hq, 128] (16-byte aligned; out may be q). Query head h reads kv head
+ * it. q, out: fp16 [B, Hq, 128] (16-byte aligned; out may be q, but no other part of it). Query head h reads kv head
  * h / (Hq / Hkv);
  *   s_j = scale * sK * sum_d q[d] * codeK[j, d],  j < seq_lens[b]
  *   out[b, h] = fp16_rn(sum_j softmax(s)_j * sV * codeV[j])
@@ -589,7 +590,7 @@ W4A8_API w4a8_status_t w4a8_kv8_attention_decode(const void* q, const w4a8_kv8_c
 /*
  * The same for several new tokens per sequence (q_start as above, required),
  * causal: row i of sequence b's n_b rows sees its tokens j < seq_lens[b] - n_b
- * + i + 1. q, out: fp16 [T, Hq, 128] (out may be q). The softmax weights are
+ * + i + 1. q, out: fp16 [T, Hq, 128] (as there). The softmax weights are
  * rounded to fp16 for the product with the values, their sum is not. workspace as for the decode call, of
  * w4a8_kv8_attention_workspace_bytes(B, T, Hq, Hkv) bytes; calls of both kinds may share one.
  */

@@ -10,6 +10,12 @@ namespace {
 
 constexpr int64_t kKv8MaxLen = int64_t(1) << 24;
 
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < static_cast<uintptr_t>(na) : x - y < static_cast<uintptr_t>(nb);
+}
+
 template <int THREADS, int VPT>
 w4a8_status_t launch_rmsnorm(const __half* X, const __half* R, const __half* W, float eps, int64_t M, int64_t K,
                              __half* H, int8_t* A8, __half* sA, int32_t* rowsum, cudaStream_t st) {
@@ -203,6 +209,7 @@ w4a8_status_t kv8_attention(const void* q, const w4a8_kv8_cache_t* c, const int3
   if (st != W4A8_OK) return st;
   if (q == nullptr || out == nullptr) return W4A8_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return W4A8_ERR_MISALIGNED;
+  if (out != q && overlap(out, T * Hq * 2 * kKv8D, q, T * Hq * 2 * kKv8D)) return W4A8_ERR_INVALID_ARG;
   const size_t parts = q_start == nullptr ? 0 : kv8_pre_part_bytes(B, T, Hq, c->Hkv);
   if (workspace == nullptr || workspace_bytes < kDecWorkspace + parts) return W4A8_ERR_WORKSPACE;
   DeviceInfo* dev = nullptr;
@@ -238,6 +245,9 @@ w4a8_status_t w4a8_rmsnorm_quantize_act(const void* X, const void* residual, con
   if (st != W4A8_OK || M == 0) return st;
   if (weight == nullptr || (residual == nullptr) != (H == nullptr) || !(eps >= 0.0f)) return W4A8_ERR_INVALID_ARG;
   if (!aligned(weight, 16) || !aligned(residual, 16) || !aligned(H, 16)) return W4A8_ERR_MISALIGNED;
+  if (H != nullptr && ((H != X && overlap(H, 2 * M * K, X, 2 * M * K)) ||
+                       (H != residual && overlap(H, 2 * M * K, residual, 2 * M * K))))
+    return W4A8_ERR_INVALID_ARG;
   const __half* x = static_cast<const __half*>(X);
   const __half* r = static_cast<const __half*>(residual);
   const __half* w = static_cast<const __half*>(weight);
@@ -268,6 +278,7 @@ w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cache_t* cach
   if (st != W4A8_OK) return st;
   if (qkv == nullptr || q_out == nullptr || (rotary_dim > 0 && inv_freq == nullptr)) return W4A8_ERR_INVALID_ARG;
   if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(inv_freq, 4)) return W4A8_ERR_MISALIGNED;
+  if (overlap(q_out, T * Hq * 2 * kKv8D, qkv, T * (Hq + 2 * cache->Hkv) * 2 * kKv8D)) return W4A8_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;
   st = device_info(&dev);
   if (st != W4A8_OK) return st;
