@@ -3,9 +3,10 @@
 Usage: python -m w4a8_quantized_gemm_quantize_b200.build [--force] [--verbose] [--debug]
 
 --debug builds libw4a8_debug.so instead: the same library compiled with
-W4A8_DEBUG, whose kernels check every global store and workspace access
-against its buffer's extent and report a failed check in the device error
-word (W4A8_DEVERR_BOUNDS) instead of performing the access.
+W4A8_DEBUG, whose GEMM, chain, KV8 append and attention kernels check every
+global store and workspace access against its buffer's extent and report a
+failed check in the device error word (W4A8_DEVERR_BOUNDS) instead of
+performing the access.
 
 The shared library links the CUDA runtime statically and resolves the one
 driver entry point it needs (cuTensorMapEncodeTiled) at run time, so it

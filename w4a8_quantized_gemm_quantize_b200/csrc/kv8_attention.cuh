@@ -186,6 +186,11 @@ __device__ __forceinline__ __half2 dec_pack(float2 o, float l) {
   return __floats2half2_rn(o.x * r, o.y * r);
 }
 
+// Debug builds: whether 128 values of q or out from offset `at` on are there.
+__device__ __forceinline__ bool kv8_row_ok(const Kv8AttnArgs& a, int64_t at) {
+  return in_bounds(at >= 0 && at <= (static_cast<int64_t>(a.s.T) * a.Hq - 1) * kKv8D, a.err);
+}
+
 // Where row R of a sequence's kv head lies in q and out.
 __device__ __forceinline__ int64_t dec_row(const Kv8AttnArgs& a, const DecPair& p, int G, int kvh, int R) {
   return ((static_cast<int64_t>(p.row0) + R / G) * a.Hq + kvh * G + R % G) * kKv8D;
@@ -522,7 +527,9 @@ __global__ void __launch_bounds__(DecCfg<DUP>::kWarps * 32, 1)
       for (int k = 0; k < 2; ++k) {
         const int col = 2 * c + k;
         if (r0 + col < cur.n * G && (!DUP || c < 2)) {
-          __half* dst = a.out + dec_row(a, cur, G, cur.j / groups, r0 + col) + 16 * g;
+          const int64_t at = dec_row(a, cur, G, cur.j / groups, r0 + col);
+          if (!kv8_row_ok(a, at)) continue;
+          __half* dst = a.out + at + 16 * g;
           const float r = l[k] > 0.0f ? 1.0f / l[k] : 0.0f;
           uint4 y[2];
           __half2* hv = reinterpret_cast<__half2*>(y);
@@ -590,7 +597,8 @@ __global__ void __launch_bounds__(DecCfg<DUP>::kWarps * 32, 1)
         o.y = fmaf(v.y, f, o.y);
       }
       if (whole) {
-        *reinterpret_cast<__half2*>(a.out + dec_row(a, p, G, p.j / groups, r0 + col) + d) = dec_pack(o, l);
+        const int64_t at = dec_row(a, p, G, p.j / groups, r0 + col);
+        if (kv8_row_ok(a, at)) *reinterpret_cast<__half2*>(a.out + at + d) = dec_pack(o, l);
       } else {
         float* part = slot_of(p, static_cast<int>(blockIdx.x));
         if (d == 0) {
@@ -615,7 +623,10 @@ __global__ void __launch_bounds__(DecCfg<DUP>::kWarps * 32, 1)
     const int e = t == 0 ? crossing[0] : crossing[1];
     if (e >= 0) {
       const int c0 = owner(s_pairs[e].first), c1 = owner(s_pairs[e].first + s_pairs[e].tiles - 1);
-      last = atom_add_relaxed_gpu(args.count + c0, 1) == c1 - c0 ? 1 : 0;
+      last = in_bounds(c0 >= 0 && c0 <= c1 && c1 < static_cast<int>(gridDim.x) && gridDim.x <= kDecMaxCtas, a.err) &&
+                     atom_add_relaxed_gpu(args.count + c0, 1) == c1 - c0
+                 ? 1
+                 : 0;
     }
     s_last[t] = last;
   }
@@ -638,7 +649,8 @@ __global__ void __launch_bounds__(DecCfg<DUP>::kWarps * 32, 1)
         dec_join(m, l, o, __ldcg(part + col), __ldcg(part + kDecCols + col),
                  __ldcg(reinterpret_cast<const float2*>(part + 2 * kDecCols + col * kKv8D + d)));
       }
-      *reinterpret_cast<__half2*>(a.out + dec_row(a, p, G, p.j / groups, r0 + col) + d) = dec_pack(o, l);
+      const int64_t at = dec_row(a, p, G, p.j / groups, r0 + col);
+      if (kv8_row_ok(a, at)) *reinterpret_cast<__half2*>(a.out + at + d) = dec_pack(o, l);
     }
     if (t == 0) args.count[c0] = 0;
   }

@@ -283,6 +283,9 @@ __device__ __forceinline__ void kv8_rotate_q(const Kv8AppendArgs& a, int64_t cap
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(o[2 * j], o[2 * j + 1]);
         __half* to = dst + (k * a.Hq + (v >> 4)) * kKv8D;
+        if (!in_bounds(row0 + k < a.s.T && (v >> 4) < a.Hq && lane.lo >= 0 && lane.lo + 4 <= kKv8D && lane.hi >= 0 &&
+                           lane.hi + 4 <= kKv8D, a.err))
+          continue;
         *reinterpret_cast<uint2*>(to + lane.lo) = w[0];
         *reinterpret_cast<uint2*>(to + lane.hi) = w[1];
       }
@@ -400,6 +403,9 @@ __global__ void __launch_bounds__(kv8_append_threads(PAGE), kv8_append_blocks(PA
       float u[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) u[e] = quotient(x[p][e], s_new, r);
+      if (!in_bounds(j >= 0 && j < P && block >= 0 && block < static_cast<int64_t>(a.c.num_pages) * heads2 &&
+                         lane.lo >= 0 && lane.lo + 4 <= kKv8D && lane.hi >= 0 && lane.hi + 4 <= kKv8D, a.err))
+        continue;
       // (|u| <= 127 (1 + 2^-22): no code is beyond 127)
       *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.lo) = pack_codes(u, 1.0f);
       *reinterpret_cast<uint32_t*>(codes + j * kKv8D + lane.hi) = pack_codes(u + 4, 1.0f);
@@ -408,6 +414,7 @@ __global__ void __launch_bounds__(kv8_append_threads(PAGE), kv8_append_blocks(PA
   if (lo > 0 && s_new > s_old) {  // the codes that were there, carried over to the larger scale
     const float ratio = __fdiv_rn(s_old, s_new);
     for (int v = t; v < lo * 16; v += kThreads) {
+      if (!in_bounds(v < P * 16 && block < static_cast<int64_t>(a.c.num_pages) * heads2, a.err)) break;
       uint2* at = reinterpret_cast<uint2*>(codes) + v;
       const uint2 c = *at;
       uint32_t w[2] = {c.x, c.y}, u[2] = {0u, 0u};
@@ -419,7 +426,8 @@ __global__ void __launch_bounds__(kv8_append_threads(PAGE), kv8_append_blocks(PA
       *at = make_uint2(u[0], u[1]);
     }
   }
-  if (t == 0) a.c.scales[block] = s_new;
+  if (t == 0 && in_bounds(block >= 0 && block < static_cast<int64_t>(a.c.num_pages) * heads2, a.err))
+    a.c.scales[block] = s_new;
 }
 
 }  // namespace w4a8

@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8PrefillA
     const int r = row0 + t;
     if (split == 0 && t < 2 * kPreRows && r < rows) {
       uint4* dst = reinterpret_cast<uint4*>(a.out + ((static_cast<int64_t>(first) + r / G) * a.Hq + kvh * G + r % G) * kKv8D);
-      for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (kv8_row_ok(a, (static_cast<int64_t>(first) + r / G) * a.Hq * kKv8D))
+        for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
     }
     return;
   }
@@ -411,11 +412,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv8_prefill_kernel(Kv8PrefillA
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
       const int64_t part_row =
           ((static_cast<int64_t>(slot) * a.c.Hkv + kvh) * args.splits + split) * (2 * kPreRows) + blk * kPreRows + lr;
-      if (CUT && !whole && half == 0) *reinterpret_cast<float2*>(args.part_ml + 2 * part_row) = make_float2(ref, l);
+      const bool part_ok = !CUT || whole ||
+                           in_bounds(part_row >= 0 && slot >= 0 && slot < args.slots && split < args.splits, a.err);
+      const bool out_ok = at < 0 || kv8_row_ok(a, at - 64 * half);
+      if (CUT && !whole && part_ok && half == 0) *reinterpret_cast<float2*>(args.part_ml + 2 * part_row) = make_float2(ref, l);
 #pragma unroll 1
       for (int q = 0; q < 2; ++q) {
         uint32_t r[32];
         tmem_ld_32_wait(tO + 32 * q, r);
+        if (!part_ok || !out_ok) continue;
         if (CUT && !whole) {
           float4* dst = reinterpret_cast<float4*>(args.part + part_row * kKv8D + 64 * half + 32 * q);
 #pragma unroll
@@ -618,6 +623,7 @@ __global__ void __launch_bounds__(kPreJoinWarps * 32) kv8_prefill_join_kernel(co
   const int tiles = (sq.pos0 + last / G + kPreTile) / kPreTile, chunk = pre_chunk(tiles, args.splits);
   if (chunk >= tiles) return;  // not cut
   const int limit = sq.pos0 + ti + 1;
+  if (!in_bounds(slot >= 0 && slot < args.slots && (limit - 1) / (chunk * kPreTile) < args.splits, a.err)) return;
   const int64_t row0 = (static_cast<int64_t>(slot) * a.c.Hkv + kvh) * args.splits * (2 * kPreRows) + row - piece_row0;
   float m = -INFINITY, l = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

@@ -32,7 +32,7 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 }
 
 // Debug builds (-DW4A8_DEBUG): every global store and workspace access of
-// the GEMM, the chain and the quantizers is checked against its buffer's
+// the GEMM, the chain, the KV8 append and attention is checked against its buffer's
 // extent; a failed check records W4A8_DEVERR_BOUNDS in the device error word
 // and the access is skipped (no trap). Release builds compile the checks away.
 constexpr int kErrBounds = 10;  // W4A8_DEVERR_BOUNDS
