@@ -506,13 +506,15 @@ W4A8_API w4a8_status_t w4a8_rmsnorm_quantize_act(const void* X, const void* resi
 /*
  * Paged 8-bit KV cache. Codes are int8 [num_pages, 2, Hkv, page, 128] (128-byte
  * aligned; second index 0 = K, 1 = V), with one fp32 scale per (page, K | V,
- * head): scales [num_pages, 2, Hkv] (4-byte aligned). Value = code * scale.
+ * head): scales [num_pages, 2, Hkv] (4-byte aligned; not negative, not NaN).
+ * Value = code * scale.
  * Token p of sequence b is at place p % page of page block_table[b, p / page]
  * (int32 [B, max_blocks], 4-byte aligned); sequences may share pages that a
  * call only reads. Entries for positions at or beyond a sequence's length are
  * not looked at.
  * Limits: D == 128; page 16, 32, 64 or 128; 1 <= Hkv, Hq % Hkv == 0, Hq <=
- * 1024; max_blocks * page <= 2^24; num_pages * 2 * Hkv * page < 2^31; B <= 65535.
+ * 1024; max_blocks * page <= 2^24; num_pages * 2 * Hkv * page < 2^31; B <=
+ * 65535; T < 2^21.
  *
  * A batch is B sequences with T rows (new tokens) in all. Sequence b's rows
  * are q_start[b] .. q_start[b + 1] - 1 (int32 [B + 1], device memory, not
@@ -542,18 +544,20 @@ typedef struct {
  * head are rotated by the token's position p = seq_lens[b] - n_b + i: pairs (2
  * j, 2 j + 1) if interleaved, else (j, j + rotary_dim / 2),
  *   (a, b) -> rope_scale * (a cos t - b sin t, a sin t + b cos t),  t = p * inv_freq[j],
- * the angle exact to 2^-22 radians at every position and for |inv_freq[j]| up to 2^30 (no fp32 product of a
- * large position), its sine and cosine to 2^-23. inv_freq: fp32 [rotary_dim /
- * 2] in device memory, as scaled for long contexts by the caller; rope_scale: a factor on the rotated values
- * (1 for none).
- * q goes to q_out, fp16 [T, Hq, 128] (16-byte aligned, no part of qkv: W4A8_ERR_INVALID_ARG); k and v (as fp32, not
- * rounded in between) into the cache. In every page that gets new tokens
+ * sine and cosine of t within 2^-23 at every position and for |inv_freq[j]| up
+ * to 2^30 (no fp32 product of a large position). inv_freq: fp32 [rotary_dim /
+ * 2] in device memory, as scaled for long contexts by the caller; rope_scale: a
+ * factor on the rotated values (1 for none).
+ * q goes to q_out, fp16 [T, Hq, 128] (16-byte aligned, no part of qkv:
+ * W4A8_ERR_INVALID_ARG); k and v (as fp32, not rounded in between) into the
+ * cache. In every page that gets new tokens
  *   s' = max(s, fp32(max |new values| / 127)),  s = 0 if the page's first place is one of them
  *   codes that were there: rint(code * (s / s')) if s' > s
  *   new codes: clamp(rint(x / s'), -127, 127)   (ties to even; s' < 1e-37 gives zeros)
  * and s' becomes its scale. Places behind the new tokens are left as they are.
  * A page that gets new tokens must not be shared with another sequence of the
- * batch. Non-finite inputs are a precondition violation (that page's contents
+ * batch, nor stand twice among the pages that one sequence's new tokens go to.
+ * Non-finite inputs are a precondition violation (that page's contents
  * unspecified).
  */
 W4A8_API w4a8_status_t w4a8_kv8_rope_append(const void* qkv, const w4a8_kv8_cache_t* cache, const int32_t* seq_lens,
@@ -571,8 +575,8 @@ W4A8_API size_t w4a8_kv8_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t H
 
 /*
  * Attention of one new token per sequence over the cache that already holds
- * it. q, out: fp16 [B, Hq, 128] (16-byte aligned; out may be q, but no other part of it). Query head h reads kv head
- * h / (Hq / Hkv);
+ * it. q, out: fp16 [B, Hq, 128] (16-byte aligned; out may be q, but no other
+ * part of it: W4A8_ERR_INVALID_ARG). Query head h reads kv head h / (Hq / Hkv);
  *   s_j = scale * sK * sum_d q[d] * codeK[j, d],  j < seq_lens[b]
  *   out[b, h] = fp16_rn(sum_j softmax(s)_j * sV * codeV[j])
  * with sK, sV the scales of j's page, in fp32; seq_lens[b] == 0 gives zeros.
@@ -590,9 +594,13 @@ W4A8_API w4a8_status_t w4a8_kv8_attention_decode(const void* q, const w4a8_kv8_c
 /*
  * The same for several new tokens per sequence (q_start as above, required),
  * causal: row i of sequence b's n_b rows sees its tokens j < seq_lens[b] - n_b
- * + i + 1. q, out: fp16 [T, Hq, 128] (as there). The softmax weights are
- * rounded to fp16 for the product with the values, their sum is not. workspace as for the decode call, of
- * w4a8_kv8_attention_workspace_bytes(B, T, Hq, Hkv) bytes; calls of both kinds may share one.
+ * + i + 1. q, out: fp16 [T, Hq, 128] (as there). In a sequence with n_b * Hq /
+ * Hkv > 32 the softmax weights are rounded to fp16 (2^-11 relative at most, or half a
+ * step of fp16's subnormal values: 2^-35 of the row's largest) for the product
+ * with the values, their sum is not; in the others, as in a decode call, to
+ * 2^-22. Which one a sequence gets depends on its own rows alone. workspace
+ * as for the decode call, of w4a8_kv8_attention_workspace_bytes(B, T, Hq, Hkv)
+ * bytes; calls of both kinds may share one.
  */
 W4A8_API w4a8_status_t w4a8_kv8_attention_prefill(const void* q, const w4a8_kv8_cache_t* cache,
                                                   const int32_t* seq_lens, const int32_t* q_start, int64_t B,

@@ -825,8 +825,8 @@ def _kv8_desc(codes, scales, block_table, seq_lens, index):
 def kv8_rope_append(qkv, Hq: int, kv_codes, kv_scales, block_table, seq_lens, inv_freq, q_start=None,
                     interleaved: bool = False, rope_scale: float = 1.0, out=None):
     """Rotates q and k of qkv fp16 [T, (Hq + 2 Hkv) * 128] at their tokens'
-    positions, returns q fp16 [T, Hq, 128] and appends k and v to the paged
-    8-bit cache. seq_lens int32 [B]: each sequence's length with its new tokens;
+    positions, returns q fp16 [T, Hq, 128] (out, if given: no part of qkv) and
+    appends k and v to the paged 8-bit cache. seq_lens int32 [B]: each sequence's length with its new tokens;
     q_start int32 [B + 1]: its first new row (None: one row per sequence).
     inv_freq fp32 [rotary_dim / 2] and rope_scale as from rope_frequencies."""
     torch = _torch()
@@ -924,7 +924,8 @@ def _kv8_attention(what, q, kv_codes, kv_scales, block_table, seq_lens, scale, q
 
 def kv8_attention_decode(q, kv_codes, kv_scales, block_table, seq_lens, scale, out=None, workspace=None):
     """Attention of one new token per sequence, q fp16 [B, Hq, 128], over the
-    paged 8-bit cache that holds it (seq_lens int32 [B]) -> fp16 [B, Hq, 128].
+    paged 8-bit cache that holds it (seq_lens int32 [B]) -> fp16 [B, Hq, 128]
+    (out may be q itself).
     workspace: uint8 of kv8_decode_workspace_bytes(B, Hq, Hkv), its first
     KV8_COUNTER_BYTES zero (one per stream is kept here if none is given); calls
     that share it must not overlap on the GPU."""
@@ -937,7 +938,7 @@ def kv8_attention_prefill(q, kv_codes, kv_scales, block_table, seq_lens, q_start
     128] with sequence b's rows q_start[b] .. q_start[b + 1] - 1 (int32
     [B + 1]), over the cache that holds them (seq_lens int32 [B]) -> fp16 [T,
     Hq, 128]. workspace as for kv8_attention_decode, of
-    kv8_workspace_bytes(B, T, Hq, Hkv)."""
+    kv8_workspace_bytes(B, T, Hq, Hkv). out may be q itself."""
     if q_start is None:
         raise W4A8Error("q_start is required")
     return _kv8_attention("w4a8_kv8_attention_prefill", q, kv_codes, kv_scales, block_table, seq_lens, scale, q_start,

@@ -136,8 +136,9 @@ w4a8_status_t kv8_decode(const Kv8AttnArgs& a, DeviceInfo* dev, const w4a8_kv8_c
 }
 
 // Pieces of 256 rows of the prefill kernel (sequence b's begin at slot start_b G
-// / 256 + b), and into how many parts each is cut: as many as fill the 148 SMs
-// where the pieces fill half of them at most.
+// / 256 + b), and into how many parts each is cut: as many as fill a B200's 148
+// SMs where the pieces fill half of them at most (a number that the size of a
+// workspace follows from, which is asked for without a device).
 int64_t kv8_pre_slots(int64_t B, int64_t T, int64_t G) { return T * G / (2 * kPreRows) + B; }
 int kv8_pre_splits(int64_t slots, int64_t Hkv) {
   const int64_t n = 148 / (slots * Hkv);
