@@ -75,11 +75,12 @@ __device__ __forceinline__ bool kv8_wait(uint64_t* bar, uint32_t parity, DevErr 
 // head against G = Hq / Hkv times 512 operations. So the kernel is built around
 // loads in flight: 12 (or 8, below) warps per SM, each with its own ring of two (three)
 // tiles of 32 tokens (K and V, 8 KB) that it fills by TMA and empties by itself, no
-// warp waiting for another before the end. Measured, 64 kv heads' cache of 8
-// sequences of 2048 to 4096 tokens: 397 MB in 75 us, 5.3 TB/s; 16 sequences with 8
-// kv heads, 106 MB, 33 us: 6.4 TB/s while the tiles run, 5 us to start and 8 for
-// the last tiles and the joins. One sequence of 500 tokens: 10 us, the chain of one
-// warp's reads, products and joins. The tensor-core part is small (16 +
+// warp waiting for another before the end. Measured, replayed graphs over caches
+// larger than the L2: 64 kv heads' cache of 8 sequences of 2048 to 4096 tokens, 397
+// MB in 77 us, 5.2 TB/s; 16 sequences with 8 kv heads, 106 MB, 34 us, of which 5
+// to start and 8 for the last tiles and the joins (33 us where the L2 holds the
+// cache). One sequence of 500 tokens: 10 us, the chain of one warp's reads, products
+// and joins. The tensor-core part is small (16 +
 // 16 products of 16 x 8 x 16 per tile and 8 columns) and stays in registers:
 // S^T = K q^T has tokens as rows and query heads as its 8 columns, so that K
 // goes from its bytes to the A operand without a shuffle (the order of the
@@ -112,7 +113,7 @@ constexpr int kDecPart = kDecCols * (2 + kKv8D);  // floats of a partial result 
 constexpr int kDecMaxCtas = 256;
 
 // One CTA per SM. Up to four columns (DUP): 12 warps with two stages each (8
-// sequences of 2048 to 4096 tokens, 64 kv heads: 75 us, with 8 warps of three
+// sequences of 2048 to 4096 tokens, 64 kv heads: 76 us, with 8 warps of three
 // stages 81: the warps wait for their own chains of instructions more than for
 // the copies). Up to eight, whose partial results take twice the room: 8 warps
 // with three (16 sequences, 8 query heads a kv head: 37 us, with 10 of two 40).

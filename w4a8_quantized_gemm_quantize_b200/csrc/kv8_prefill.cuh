@@ -12,18 +12,21 @@ namespace w4a8 {
 //   P_t = 2^(z - M)    thread = row, the row of S in registers
 //   O_t += P_t V       128 x 128 x 128, P from tensor memory, V from shared
 // so that the tensor cores need 2 * 2 * 512 cycles a tile and pair of blocks,
-// and the exponentials (16 a cycle and SM) as many: those two bound it. Tensor
+// and the exponentials (16 a cycle and SM) as many: the floor of a tile. Tensor
 // memory holds O_0, O_1, P_0, P_1 and one S: a softmax reads its row of S at
 // once, and the other block's next S is made while it works, so that neither
 // block waits for its own products (with S_0 and S_1 in place of the one S, P_t
 // over S_t, each block's S, softmax and PV followed one another: 5700 cycles a
-// tile and pair of blocks instead of 4500). Measured: 1000 new tokens of 9017
-// 195 us (717 TFLOP/s), 3 prompts of 1500 to 2100 tokens 181 us (551: some 700
-// pieces of 1 to 17 tiles, whose first tile and last products nothing overlaps). The softmax bounds a tile: its warps' instructions take
-// 56 % of the issue slots, the products 40 % of the tensor pipe's cycles. Fewer
-// and longer CTAs that take one piece after another were slower (254 and 275 us
-// for 196 and 221), and so were 8 softmax warps with 128 registers a thread (222
-// for 192).
+// tile and pair of blocks instead of 4500). Measured, replayed graphs over caches
+// larger than the L2: 1000 new tokens of 9017 195 us (716 TFLOP/s), 3 prompts of 1500
+// to 2100 tokens 181 us (549: some 700 pieces of 1 to 17 tiles, whose first tile and
+// last products nothing overlaps). Nothing is full: of the cycles that an SM is
+// active the first takes 65 % of the issue slots, 44 % of the tensor pipe, 44 % of the
+// exponentials. What is left is the order of a tile: a next S waits until the
+// one S is read, a row's two threads exchange their maxima before the first
+// exponential. Fewer and longer CTAs that take one piece after another were slower
+// (254 and 275 us for 196 and 221), and so were 8 softmax warps with 128 registers
+// a thread (222 for 192).
 //
 // Roles: warps 0-15 the softmax, two threads a row (warps 8 t + 4 h ..: block t,
 // columns 64 h ..; with one thread a row and 128 values in its registers nothing
