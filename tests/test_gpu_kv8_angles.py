@@ -75,7 +75,7 @@ def test_angles_of_every_layout(interleaved, rotary, single):
         check(f, interleaved, second, single, 10 + rotary + second)
 
 
-@pytest.mark.parametrize("lo,hi", [(1e-9, 1e-6), (1e-4, 1.0), (1.0, 8.0), (8.0, 1e3), (1e3, 1e6)])
+@pytest.mark.parametrize("lo,hi", [(1e-9, 1e-6), (1e-4, 1.0), (1.0, 8.0), (8.0, 1e3), (1e3, 1e6), (1e6, 1e9)])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 def test_angles_of_any_frequency(lo, hi, sign):
     """Tiny, ordinary, above one (a base below one) and large frequencies, and turns the other way."""
